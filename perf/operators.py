@@ -1,0 +1,422 @@
+"""The rotating cache append, the 4-bit cache and the attention over it: cases, plain forms and the library's calls.
+
+Cases are of three kinds:
+
+- ``append``: queries and keys rotated to their positions, keys and values stored in a paged f32 / bf16 cache.
+- ``append4``: the same into a 4-bit cache, then the stored rows (and rows that were there before) read back as values.
+- ``attn4``: paged attention of one step over a 4-bit cache.
+
+The 4-bit cache holds, for a (block of 16 tokens, kv-head), one tile of bytes: K codes ``[16][D/2]`` (dim 2j in the low
+half of byte j), V codes ``[2][8][4][2][D/16]`` (index h, c, t, i: token 4t + 2h + i, dims c D/8 and on), K scales
+``[16][D/16]`` and V scales ``[D/16][16]``.  A code is e2m1, a scale e4m3 for 16 dims of one token; a value is
+code * scale * (the tensor's own scale).
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+# ------------------------------------------------------------------ cases
+
+def listed():
+    llama = {"hq": 32, "hkv": 8, "d": 128, "dtype": "bf16"}
+    tiny = {"hq": 32, "hkv": 4, "d": 64, "dtype": "bf16"}
+    return [
+        # one decode token of one request: nothing but latency
+        {"name": "append_one_token", "op": "append", **llama, "tokens": 1, "rotary": 128, "pairs": False, "fused": True, "padded": 0, "lens": 1},
+        # a long prompt's projections, q, k and v as slices of one [T, (Hq + 2 Hkv) D] product
+        {"name": "append_prompt_8192", "op": "append", **llama, "tokens": 8192, "rotary": 128, "pairs": False, "fused": True, "padded": 0, "lens": 2},
+        # an fp32 batch of odd size with padding rows, half of each head rotated, adjacent pairs
+        {"name": "append_f32_partial_777", "op": "append", "hq": 4, "hkv": 4, "d": 64, "dtype": "f32", "tokens": 777, "rotary": 32, "pairs": True, "fused": False, "padded": 9, "lens": 3},
+        # a decode step of 64 requests into the 4-bit cache
+        {"name": "append4_decode_64", "op": "append4", **tiny, "tokens": 64, "rotary": 64, "pairs": False, "fused": True, "padded": 0, "lens": 4},
+        # a prompt of odd length into the 4-bit cache
+        {"name": "append4_prompt_4099", "op": "append4", **llama, "tokens": 4099, "rotary": 128, "pairs": False, "fused": True, "padded": 3, "lens": 5},
+        # one short request: the smallest attention call
+        {"name": "attn4_decode_one_77", "op": "attn4", **llama, "seqs": 1, "lmin": 77, "lmax": 77, "qmin": 1, "qmax": 1, "host": True, "lens": 6},
+        # decode batches of the two attention shapes that the benchmark uses
+        {"name": "attn4_decode_64_d64", "op": "attn4", **tiny, "seqs": 64, "lmin": 128, "lmax": 2048, "qmin": 1, "qmax": 1, "host": True, "lens": 7},
+        {"name": "attn4_decode_192_d128", "op": "attn4", **llama, "seqs": 192, "lmin": 256, "lmax": 8192, "qmin": 1, "qmax": 1, "host": False, "lens": 8},
+        # few requests with long contexts: the keys of one request go over many processors
+        {"name": "attn4_decode_long_8", "op": "attn4", **llama, "seqs": 8, "lmin": 32768, "lmax": 131072, "qmin": 1, "qmax": 1, "host": True, "lens": 9},
+        # prompt chunks over cached context
+        {"name": "attn4_prefill_4x1024", "op": "attn4", **llama, "seqs": 4, "lmin": 1024, "lmax": 5120, "qmin": 1024, "qmax": 1024, "host": True, "lens": 10},
+        # a few drafted tokens of each request verified at once, lengths known on the device only
+        {"name": "attn4_verify_33", "op": "attn4", "hq": 8, "hkv": 2, "d": 64, "dtype": "bf16", "seqs": 33, "lmin": 40, "lmax": 3000, "qmin": 1, "qmax": 13, "host": False, "lens": 11},
+        # fp32 queries
+        {"name": "attn4_f32_5", "op": "attn4", "hq": 4, "hkv": 4, "d": 64, "dtype": "f32", "seqs": 5, "lmin": 30, "lmax": 900, "qmin": 1, "qmax": 30, "host": True, "lens": 12},
+    ]
+
+
+def draw(rng):
+    def log(lo, hi):
+        return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+    d = rng.choice([64, 128])
+    hq, hkv = rng.choice([(32, 8), (32, 4), (8, 2), (4, 4), (8, 1), (16, 1)])
+    c = {"hq": hq, "hkv": hkv, "d": d, "dtype": "f32" if rng.random() < 0.2 else "bf16", "lens": rng.randrange(1 << 30)}
+    kind = rng.choice(["append", "append4", "decode", "decode", "prefill"])
+    if kind in ("append", "append4"):
+        t = log(1, 8192)
+        pairs = rng.random() < 0.3
+        return {"op": kind, **c, "tokens": t, "rotary": rng.choice([32, d // 2, d]), "pairs": pairs, "fused": rng.random() < 0.7,
+                "padded": rng.randrange(0, 1 + t // 8)}
+    if kind == "decode":
+        s = log(1, 256)
+        q = rng.choice([1, 1, 1, rng.randrange(2, 17)])
+        top = min(131072, 900_000 * 8 * 128 // (s * hkv * d), 10 ** 11 // (4 * d * hq * q * s))
+        lmax = max(q, log(min(64, top), top))
+        return {"op": "attn4", **c, "seqs": s, "lmin": max(q, lmax // rng.choice([1, 4, 16])), "lmax": lmax, "qmin": 1, "qmax": q, "host": rng.random() < 0.5}
+    s = rng.randrange(1, 5)
+    q = log(70, 200 if c["dtype"] == "f32" else 1100)
+    lmax = q + log(1, max(2, min(4096, 16 * 10 ** 10 // (4 * d * hq * q * s) - q)))
+    return {"op": "attn4", **c, "seqs": s, "lmin": q, "lmax": lmax, "qmin": max(1, q // rng.choice([1, 3])), "qmax": q, "host": rng.random() < 0.5}
+
+
+def _lengths(case):
+    """(lengths, query lengths) of an attention case: the case's own, whatever the seed of its values."""
+    r = random.Random(case["lens"])
+    ql = [r.randint(case["qmin"], case["qmax"]) for _ in range(case["seqs"])]
+    return [max(q, r.randint(case["lmin"], case["lmax"])) for q in ql], ql
+
+
+def _dtype(case):
+    return torch.float32 if case["dtype"] == "f32" else torch.bfloat16
+
+
+def work(case):
+    hq, hkv, d = case["hq"], case["hkv"], case["d"]
+    e = 4 if case["dtype"] == "f32" else 2
+    if case["op"] == "attn4":
+        lens, ql = _lengths(case)
+        pairs = sum(q * (n - q) + q * (q + 1) // 2 for n, q in zip(lens, ql))
+        return {"bytes": sum(lens) * hkv * (d + d // 8) + 2 * sum(ql) * hq * d * e, "flops": 4 * d * hq * pairs}
+    t = case["tokens"]
+    kept = t - case["padded"]
+    moved = t * hq * d * e * 2 + kept * 2 * hkv * d * e + t * (4 * case["rotary"] + 16)
+    flops = 3 * case["rotary"] * (hq * t + hkv * kept)
+    if case["op"] == "append":
+        return {"bytes": moved + kept * 2 * hkv * d * e, "flops": flops}
+    rows = kept + min(kept, 256)
+    return {"bytes": moved + kept * hkv * (d + d // 8) + rows * (hkv * (d + d // 8) + 2 * hkv * d * e + 8),
+            "flops": flops + 4 * kept * hkv * d + 4 * rows * hkv * d}
+
+
+# ------------------------------------------------------------------ inputs
+
+def _tile_bytes(d):
+    return 18 * d
+
+
+def _tiles(k, v):
+    """The tiles that hold k and v, [n][16][d] each, scaled by 1."""
+    n, _, d = k.shape
+
+    def quantise(x):
+        g = x.reshape(n, 16, d // 16, 16)
+        s = (g.abs().amax(-1) / 6).clamp(max=448).to(torch.float8_e4m3fn)
+        y = g / s.float().clamp(min=2 ** -9).unsqueeze(-1)
+        return _codes(y).reshape(n, 16, d // 2, 2), s.view(torch.uint8)
+
+    ck, sk = quantise(k)
+    cv, sv = quantise(v)
+    bk = ck[..., 0] | (ck[..., 1] << 4)
+    bv = (cv[..., 0] | (cv[..., 1] << 4)).reshape(n, 4, 2, 2, 8, d // 16).permute(0, 2, 4, 1, 3, 5)
+    return torch.cat([bk.reshape(n, -1), bv.reshape(n, -1), sk.reshape(n, -1), sv.transpose(1, 2).reshape(n, -1)], 1)
+
+
+def _codes(y):
+    """e2m1 codes (uint8) of y, to the nearest, ties to the even code."""
+    a = y.abs()
+    c = (a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5)
+    return c | (torch.signbit(y).to(torch.uint8) << 3)
+
+
+def _pool(blocks, hkv, d, gen):
+    """A 4-bit pool of normal keys and values, a few key channels larger than the rest as rotated keys have them."""
+    base = min(blocks * hkv, 16384)
+    k = torch.randn(base, 16, d, device="cuda", generator=gen)
+    k *= 1 + 3 * (torch.rand(d, device="cuda", generator=gen) < 0.05)
+    tiles = _tiles(k, torch.randn(base, 16, d, device="cuda", generator=gen))
+    if base < blocks * hkv:
+        tiles = tiles[torch.randint(0, base, (blocks * hkv,), device="cuda", generator=gen)]
+    return tiles.reshape(blocks, hkv, _tile_bytes(d))
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(int(seed) * 7919 + case["lens"] % 7919)
+    hq, hkv, d, dt = case["hq"], case["hkv"], case["d"], _dtype(case)
+
+    def normal(*shape):
+        return torch.randn(*shape, device="cuda", generator=gen).to(dt)
+
+    if case["op"] == "attn4":
+        lens, ql = _lengths(case)
+        held = [-(-n // 16) for n in lens]
+        blocks, wide, s = sum(held) + 3, max(held), len(lens)
+        order = torch.randperm(blocks, device="cuda", generator=gen).to(torch.int32)
+        starts = torch.tensor([sum(held[:i]) for i in range(s)])
+        at = starts[:, None] + torch.arange(wide)
+        at = torch.where(torch.arange(wide) < torch.tensor(held)[:, None], at, 0)
+        begins = [0]
+        for q in ql:
+            begins.append(begins[-1] + q)
+        st = {"case": case, "q": normal(begins[-1], hq, d), "cache": _pool(blocks, hkv, d, gen), "tables": order[at.cuda()].contiguous(),
+              "lens": torch.tensor(lens, dtype=torch.int32, device="cuda"), "begins": torch.tensor(begins, dtype=torch.int32, device="cuda"),
+              "qmax": max(ql), "lmax": max(lens), "scale": d ** -0.5, "k_scale": 0.75, "v_scale": 1.5, "plan": None}
+        if case["host"]:
+            st["lens_host"], st["begins_host"] = st["lens"].cpu().numpy(), st["begins"].cpu().numpy()
+        st["out"] = torch.empty_like(st["q"])
+        if own:
+            from paged_kv_cache_469_b200 import lib
+            st["workspace"] = lib.new_fp4_workspace(s, hq, hkv, d, st["lmax"])
+        return st
+
+    t, r = case["tokens"], case["rotary"]
+    if case["fused"]:
+        qkv = normal(t, (hq + 2 * hkv) * d)
+        q, k, v = (x.unflatten(1, (-1, d)) for x in qkv.split([hq * d, hkv * d, hkv * d], dim=1))
+    else:
+        q, k, v = normal(t, hq, d), normal(t, hkv, d), normal(t, hkv, d)
+    longest = 32768
+    angle = torch.arange(longest, dtype=torch.float64, device="cuda")[:, None] * 10000.0 ** (-torch.arange(0, r, 2, device="cuda", dtype=torch.float64) / r)
+    blocks = -(-t // 16) * 2 + 4
+    order = torch.randperm(blocks, device="cuda", generator=gen)
+    first = int(torch.randint(0, longest - t, (1,), generator=gen, device="cuda"))
+    at = torch.arange(t, device="cuda")
+    slots = order[at // 16] * 16 + at % 16
+    if t <= 256:  # decodes: every token in a block of its own, at any place of it
+        order = torch.randperm(blocks + t, device="cuda", generator=gen)
+        blocks += t
+        slots = order[at] * 16 + torch.randint(0, 16, (t,), device="cuda", generator=gen)
+        positions = torch.randint(0, longest, (t,), device="cuda", generator=gen)
+    else:
+        positions = first + at
+    pads = case["padded"]
+    if pads:
+        slots[t - pads:] = -1
+        positions[t - pads:] = 0
+    st = {"case": case, "q": q, "k": k, "v": v, "slots": slots, "positions": positions, "q_out": torch.empty(t, hq, d, dtype=dt, device="cuda"),
+          "cos_sin": torch.cat([angle.cos(), angle.sin()], 1).float(), "k_scale": 0.75, "v_scale": 1.5}
+    if case["op"] == "append":
+        st["k_cache"], st["v_cache"] = normal(blocks, hkv, 16, d), normal(blocks, hkv, 16, d)
+    else:
+        st["cache"] = _pool(blocks, hkv, d, gen)
+        kept = slots[:t - pads]
+        # the rows just stored, and up to 256 other tokens of the same blocks
+        st["read"] = torch.cat([kept, kept[:256] ^ 1]).contiguous()
+        n = st["read"].numel()
+        st["k_read"], st["v_read"] = (torch.empty(n, hkv, d, dtype=dt, device="cuda") for _ in range(2))
+    return st
+
+
+# ------------------------------------------------------------------ one pass
+
+def run(st):
+    return (_run_own if own else _run_plain)(st)
+
+
+def _run_own(st):
+    from paged_kv_cache_469_b200 import lib
+    c = st["case"]
+    if c["op"] == "attn4":
+        return lib.attention_varlen_fp4(st["out"], st["q"], st["cache"], st["tables"], st["lens"], st["begins"], max_query_len=st["qmax"],
+                                        max_seq_len=st["lmax"], scale=st["scale"], k_scale=st["k_scale"], v_scale=st["v_scale"],
+                                        workspace=st["workspace"], seq_lens_host=st.get("lens_host"), query_start_loc_host=st.get("begins_host"))
+    if c["op"] == "append":
+        lib.rope_append(st["q"], st["k"], st["v"], st["k_cache"], st["v_cache"], st["slots"], st["positions"], st["cos_sin"], q_out=st["q_out"],
+                        interleaved=c["pairs"])
+        return st["q_out"], st["k_cache"], st["v_cache"]
+    lib.rope_append_fp4(st["q"], st["k"], st["v"], st["cache"], st["slots"], st["positions"], st["cos_sin"], k_scale=st["k_scale"],
+                        v_scale=st["v_scale"], q_out=st["q_out"], interleaved=c["pairs"])
+    lib.gather_fp4(st["cache"], st["read"], k_scale=st["k_scale"], v_scale=st["v_scale"], k_out=st["k_read"], v_out=st["v_read"])
+    return st["q_out"], st["k_read"], st["v_read"]
+
+
+def _rotate(x, cos, sin, pairs):
+    x = x.float()
+    r = 2 * cos.shape[-1]
+    cos, sin = cos[:, None], sin[:, None]
+    a, b = (x[..., 0:r:2], x[..., 1:r:2]) if pairs else (x[..., :r // 2], x[..., r // 2:r])
+    ya, yb = a * cos - b * sin, b * cos + a * sin
+    y = torch.stack([ya, yb], -1).flatten(-2) if pairs else torch.cat([ya, yb], -1)
+    return torch.cat([y, x[..., r:]], -1)
+
+
+def _values(raw, d):
+    """K and V, [...][16][d] in fp32, of tiles [...][18 d] of bytes, scaled by 1."""
+    lead = raw.shape[:-1]
+    table = torch.tensor(E2M1 + tuple(-x for x in E2M1), device=raw.device)
+    kc, vc, ks, vs = raw.split([8 * d, 8 * d, d, d], -1)
+
+    def codes(b):
+        return table[torch.stack([b & 15, b >> 4], -1).flatten(-2).int()]
+
+    n = len(lead)
+    k = codes(kc).reshape(*lead, 16, d // 16, 16)
+    v = codes(vc.reshape(*lead, 2, 8, 4, 2, d // 16).permute(*range(n), n + 2, n, n + 3, n + 1, n + 4).reshape(*lead, 16, d // 2))
+    k = k * ks.contiguous().view(torch.float8_e4m3fn).float().reshape(*lead, 16, d // 16, 1)
+    v = v.reshape(*lead, 16, d // 16, 16) * vs.contiguous().view(torch.float8_e4m3fn).float().reshape(*lead, d // 16, 16).transpose(-1, -2).unsqueeze(-1)
+    return k.flatten(-2), v.flatten(-2)
+
+
+def _store4(cache, rows_k, rows_v, slots, k_scale, v_scale):
+    """Rows [n][hkv][d] in fp32 into the tiles of their slots."""
+    n, hkv, d = rows_k.shape
+
+    def quantise(x, g):
+        x = x.reshape(n, hkv, d // 16, 16)
+        s = (x.abs().amax(-1) / torch.full((), 6 * g, device=x.device)).clamp(max=448).to(torch.float8_e4m3fn)
+        y = x / torch.where(s.float() > 0, s.float() * g, torch.inf).unsqueeze(-1)
+        c = _codes(y).reshape(n, hkv, d // 2, 2)
+        return c[..., 0] | (c[..., 1] << 4), s.view(torch.uint8)
+
+    kb, ks = quantise(rows_k, k_scale)
+    vb, vs = quantise(rows_v, v_scale)
+    blk, off = slots // 16, slots % 16
+    kc, vc, sk, sv = cache.split([8 * d, 8 * d, d, d], -1)
+    kc.unflatten(-1, (16, d // 2))[blk, :, off] = kb
+    t, h, i = off // 4, off // 2 % 2, off % 2
+    vc.unflatten(-1, (2, 8, 4, 2, d // 16)).permute(0, 2, 4, 5, 1, 3, 6)[blk, h, t, i] = vb.unflatten(-1, (8, d // 16))
+    sk.unflatten(-1, (16, d // 16))[blk, :, off] = ks
+    sv.unflatten(-1, (d // 16, 16)).permute(0, 3, 1, 2)[blk, off] = vs
+
+
+def _run_plain(st):
+    c = st["case"]
+    if c["op"] == "attn4":
+        return _attend(st)
+    table = st["cos_sin"][st["positions"]]
+    half = table.shape[1] // 2
+    cos, sin = table[:, :half], table[:, half:]
+    dt = st["q_out"].dtype
+    st["q_out"].copy_(_rotate(st["q"], cos, sin, c["pairs"]))
+    keep = st["slots"] >= 0
+    slots = st["slots"][keep]
+    k, v = _rotate(st["k"], cos, sin, c["pairs"])[keep], st["v"][keep]
+    if c["op"] == "append":
+        blk, off = slots // 16, slots % 16
+        st["k_cache"][blk, :, off] = k.to(dt)
+        st["v_cache"][blk, :, off] = v
+        return st["q_out"], st["k_cache"], st["v_cache"]
+    _store4(st["cache"], k, v.float(), slots, st["k_scale"], st["v_scale"])
+    blk, off = st["read"] // 16, st["read"] % 16
+    tiles = st["cache"][blk]
+    kr, vr = _values(tiles, c["d"])
+    at = off[:, None, None, None].expand(-1, c["hkv"], 1, c["d"])
+    return (st["q_out"], (kr.gather(2, at).squeeze(2) * st["k_scale"]).to(dt), (vr.gather(2, at).squeeze(2) * st["v_scale"]).to(dt))
+
+
+def _attend(st):
+    c = st["case"]
+    hq, hkv, d = c["hq"], c["hkv"], c["d"]
+    g, s, lmax, qmax = hq // hkv, st["lens"].shape[0], st["tables"].shape[1] * 16, st["qmax"]
+    ql = (st["begins"][1:] - st["begins"][:-1]).long()
+    j = torch.arange(qmax, device="cuda")
+    row = (st["begins"][:-1].long()[:, None] + j).clamp(max=st["q"].shape[0] - 1)
+    q = st["q"].float()[row].reshape(s, qmax, hkv, g, d).permute(0, 2, 3, 1, 4).reshape(s, hkv, g * qmax, d)
+    k, v = _values(st["cache"][st["tables"]], d)
+    k = k.transpose(1, 2).reshape(s, hkv, lmax, d) * st["k_scale"]
+    v = v.transpose(1, 2).reshape(s, hkv, lmax, d) * st["v_scale"]
+    last = (st["lens"].long() - ql)[:, None] + j
+    x = q @ k.transpose(-1, -2) * st["scale"]
+    seen = torch.arange(lmax, device="cuda") <= torch.minimum(last, st["lens"].long()[:, None] - 1)[..., None]
+    x = x.reshape(s, hkv, g, qmax, lmax).masked_fill(~seen[:, None, None], -torch.inf)
+    x = torch.exp(x - x.amax(-1, keepdim=True))
+    x = (x / x.sum(-1, keepdim=True)).reshape(s, hkv, g * qmax, lmax)
+    o = (x @ v).reshape(s, hkv, g, qmax, d).permute(0, 3, 1, 2, 4).reshape(s * qmax, hq, d)
+    # the rows of each sequence's own queries, in order
+    token = torch.arange(st["q"].shape[0], device="cuda")
+    seq = torch.searchsorted(st["begins"][1:].long(), token, right=True)
+    return o[seq * qmax + token - st["begins"].long()[seq]].to(st["q"].dtype)
+
+
+# ------------------------------------------------------------------ in 64 bits
+
+def _f64_tables():
+    e2 = torch.tensor(E2M1, dtype=torch.float64, device="cuda")
+    b = torch.arange(127, device="cuda")
+    e, m = (b >> 3).double(), (b & 7).double()
+    e4 = torch.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e - 10))
+    return torch.cat([e2, -e2]), e4
+
+
+def _nearest(x, grid):
+    """Index of the nearest of the ascending `grid` to each x >= 0, ties to the even index; past the end, the last."""
+    hi = torch.searchsorted(grid, x.contiguous()).clamp(1, len(grid) - 1)
+    lo = hi - 1
+    below, above = x - grid[lo], grid[hi] - x
+    return torch.where((above < below) | ((above == below) & (hi % 2 == 0)), hi, lo)
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    e2, e4 = _f64_tables()
+    hq, hkv, d = case["hq"], case["hkv"], case["d"]
+    if case["op"] == "attn4":
+        lens, ql = _lengths(case)
+        if 4.0 * d * hq * sum(a * b for a, b in zip(lens, ql)) > 2e13:
+            return None
+        outs, at = [], 0
+        for s, (n, q) in enumerate(zip(lens, ql)):
+            tiles = st["cache"][st["tables"][s, :-(-n // 16)].long()].transpose(0, 1)
+            k, v = (x.reshape(hkv, -1, d)[:, :n] for x in _f64_values(tiles, d, e2, e4))
+            rows = st["q"][at:at + q].double().reshape(q, hkv, hq // hkv, d).permute(1, 2, 0, 3)
+            x = torch.einsum("hgqd,hnd->hgqn", rows, k * st["k_scale"]) * st["scale"]
+            future = torch.ones(q, n, dtype=torch.bool, device="cuda").triu(n - q + 1)
+            p = torch.softmax(x.masked_fill(future, -torch.inf), -1)
+            outs.append(torch.einsum("hgqn,hnd->qhgd", p, v * st["v_scale"]).reshape(q, hq, d))
+            at += q
+        return torch.cat(outs)
+    r, pairs, t = case["rotary"], case["pairs"], case["tokens"]
+    i = torch.arange(r, device="cuda")
+    angle, mate = (i // 2, i ^ 1) if pairs else (i % (r // 2), (i + r // 2) % r)
+    sign = torch.where((i % 2 == 0) if pairs else (i < r // 2), -1.0, 1.0).double()
+    cs = st["cos_sin"].double()[st["positions"]]
+    cos, sin = cs[:, angle][:, None], (cs[:, angle + r // 2] * sign)[:, None]
+
+    def turned(x):
+        y = x.double().clone()
+        y[..., :r] = y[..., :r] * cos + y[..., :r][..., mate] * sin
+        return y
+
+    kept = t - case["padded"]
+    slots = st["slots"][:kept]
+    q, k, v = turned(st["q"]), turned(st["k"])[:kept], st["v"].double()[:kept]
+    if case["op"] == "append":
+        kc, vc = st["k_cache"].double().transpose(1, 2).flatten(0, 1), st["v_cache"].double().transpose(1, 2).flatten(0, 1)
+        kc[slots], vc[slots] = k, v
+        return q, kc.unflatten(0, (-1, 16)).transpose(1, 2).contiguous(), vc.unflatten(0, (-1, 16)).transpose(1, 2).contiguous()
+
+    def held(x, g):
+        x = x.unflatten(-1, (-1, 16))
+        s = e4[_nearest(x.abs().amax(-1) / (6 * g), e4)].unsqueeze(-1)
+        y = e2[_nearest((x / torch.where(s > 0, s * g, torch.inf)).abs(), e2[:8])]
+        return (torch.copysign(y, x) * s * g).flatten(-2)
+
+    outs = []
+    for old, new, g in zip(_f64_values(st["cache"], d, e2, e4), (k, v), (st["k_scale"], st["v_scale"])):
+        rows = old.transpose(1, 2).flatten(0, 1) * g
+        rows[slots] = held(new, g)
+        outs.append(rows[st["read"]])
+    return (q, *outs)
+
+
+def _f64_values(tiles, d, e2, e4):
+    """K and V of tiles [a][b][18 d], [a][b][16][d] in fp64, scaled by 1: every element read from its own place."""
+    token, dim = torch.arange(16, device="cuda")[:, None], torch.arange(d, device="cuda")
+    wide = d // 8  # dims of one token in a chunk of V
+    v_byte = 8 * d + ((((token // 2 % 2) * 8 + dim // wide) * 4 + token // 4) * 2 + token % 2) * (wide // 2) + dim % wide // 2
+    k_byte = token * (d // 2) + dim // 2
+    half = 4 * (dim % 2)
+
+    def value(code, scale):
+        return e2[tiles[..., code].int() >> half & 15] * e4[tiles[..., scale].int()]
+
+    return value(k_byte, 16 * d + token * (d // 16) + dim // 16), value(v_byte, 17 * d + dim // 16 * 16 + token)
