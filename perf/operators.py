@@ -175,7 +175,7 @@ def prepare(case, seed):
         st["out"] = torch.empty_like(st["q"])
         if own:
             from paged_kv_cache_469_b200 import lib
-            st["workspace"] = lib.new_fp4_workspace(s, hq, hkv, d, st["lmax"])
+            st["workspace"] = lib.new_fp4_workspace(s, begins[-1], hq, hkv, d)
         return st
 
     t, r = case["tokens"], case["rotary"]
