@@ -337,6 +337,123 @@ int pa_plan_step(const int32_t* free_queue, int queue_len, int32_t* planner_stat
                  int32_t* seq_lens, int32_t* query_start_loc, int64_t* slot_mapping,
                  int max_tokens, struct CUstream_st* stream);
 
+/*
+ * pa_rope_append -- rotate a step's queries and keys to their positions and
+ * write the keys and values into their cache slots, in one launch.
+ *
+ * For every token i with position p = positions[i] (a row of cos_sin):
+ *   q_out[i][h] = R(p) q[i][h]                     every q-head h
+ *   k_cache[slot / 16][h][slot % 16] = R(p) k[i][h]  every kv-head h, where
+ *   v_cache[slot / 16][h][slot % 16] = v[i][h]       slot = slot_mapping[i]
+ * R(p) turns the first rotary_dim dims, in pairs (x1, x2) by the angle whose
+ * cosine and sine are cos_sin[p][j] and cos_sin[p][rotary_dim / 2 + j]:
+ *   y1 = x1 cos - x2 sin,   y2 = x2 cos + x1 sin
+ * Pair j is dims (j, j + rotary_dim / 2), or (2 j, 2 j + 1) when interleaved.
+ * Dims from rotary_dim on, and V, are copied bit-exactly; rotary_dim 0 rotates
+ * nothing (positions and cos_sin may be NULL).  The rotation is computed in
+ * fp32, every product and sum rounded on its own, and rounded once to dtype.
+ *
+ * A slot outside the pool (a padding row) skips the cache write; the query is
+ * rotated all the same.  A position outside [0, max_position) leaves the token
+ * out: none of its rows is written.  Two tokens naming one slot race (caller
+ * error).
+ *
+ *   q_out         [num_tokens][num_q_heads][head_dim] (written); q itself when q
+ *                 is contiguous, else apart from q, k and v
+ *   q, k, v       rows of [heads][head_dim], consecutive tokens q_stride,
+ *                 k_stride, v_stride elements apart (a multiple of 16 bytes;
+ *                 slices of one fused projection need no copy)
+ *   k_cache,
+ *   v_cache       [num_blocks][num_kv_heads][block_size][head_dim] (written)
+ *   slot_mapping,
+ *   positions     int64 [num_tokens]
+ *   cos_sin       fp32 [max_position][rotary_dim], 16-byte aligned
+ * num_q_heads may be 0 (q and q_out NULL).  Supported: rotary_dim a multiple of
+ * 16 up to head_dim; head_dim in {64, 128}; block_size 16; dtype f32 or bf16.
+ */
+int pa_rope_append(void* q_out, const void* q, int64_t q_stride, const void* k,
+                   int64_t k_stride, const void* v, int64_t v_stride, void* k_cache,
+                   void* v_cache, const int64_t* slot_mapping, const int64_t* positions,
+                   const float* cos_sin, int64_t max_position, int rotary_dim, int interleaved,
+                   int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                   int block_size, int num_blocks, pa_dtype dtype, struct CUstream_st* stream);
+
+/*
+ * The 4-bit cache.  kv_cache holds K and V: uint8
+ * [num_blocks][num_kv_heads][18 * head_dim], 16-byte aligned; the tile of one
+ * (block, kv-head) is
+ *   K codes   [16 tokens][head_dim / 2]       dim 2j in the low half of byte j
+ *   V codes   [2 h][8 c][4 t][2 i][head_dim / 16]   token 4 t + 2 h + i, dims
+ *             c * head_dim / 8 on, two to a byte as in K
+ *   K scales  [16 tokens][head_dim / 16]
+ *   V scales  [head_dim / 16][16 tokens]
+ * A code is e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 by its low three bits, negative
+ * with the fourth.  A scale is an e4m3 byte for 16 neighbouring dims of one
+ * token.  Value = code * scale * k_scale (v_scale), the last one fp32 number
+ * per tensor that the caller keeps: 4.5 bits a value, 3.6 times less than bf16.
+ */
+
+/*
+ * pa_rope_append_fp4 -- pa_rope_append into a 4-bit cache.  Each 16 dims x of a
+ * token's rotated K row, or V row, are stored as
+ *   scale = e4m3(min(max|x| / (6 k_scale), 448))     round to nearest even
+ *   code  = e2m1(x / (scale * k_scale))              nearest even, at most 6
+ * (all codes 0 when the scale rounds to 0, i.e. below 2^-10).  A NaN makes its
+ * group's scale NaN; infinities count as the largest value.
+ * The bytes of other tokens of a block are left as they are.
+ * Arguments as pa_rope_append's; k_scale, v_scale positive and finite.
+ * Supported: as pa_rope_append, but rotary_dim a multiple of 32 unless
+ * interleaved.
+ */
+int pa_rope_append_fp4(void* q_out, const void* q, int64_t q_stride, const void* k,
+                       int64_t k_stride, const void* v, int64_t v_stride, void* kv_cache,
+                       float k_scale, float v_scale, const int64_t* slot_mapping,
+                       const int64_t* positions, const float* cos_sin, int64_t max_position,
+                       int rotary_dim, int interleaved, int num_tokens, int num_q_heads,
+                       int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                       pa_dtype dtype, struct CUstream_st* stream);
+
+/*
+ * pa_gather_fp4 -- rows of a 4-bit cache as values: for every i < num_rows with
+ * slots[i] in the pool, k_out[i][h][:] and v_out[i][h][:] are the values of that
+ * slot's K and V rows, rounded once to dtype.  Rows of other slots are left as
+ * they are.
+ *   k_out, v_out  [num_rows][num_kv_heads][head_dim] (written)
+ *   slots         int64 [num_rows]
+ */
+int pa_gather_fp4(void* k_out, void* v_out, const void* kv_cache, float k_scale, float v_scale,
+                  const int64_t* slots, int num_rows, int num_kv_heads, int head_dim,
+                  int block_size, int num_blocks, pa_dtype dtype, struct CUstream_st* stream);
+
+/*
+ * Bytes of workspace pa_attention_varlen_fp4 needs for a step of at most
+ * num_seqs sequences and num_tokens query tokens.  0 means invalid arguments.
+ * Zero it once (pa_workspace_init); its first word is the status word that
+ * pa_workspace_status reads.
+ */
+size_t pa_attention_fp4_workspace_size(int num_seqs, int num_tokens, int num_q_heads,
+                                       int num_kv_heads, int head_dim);
+
+/*
+ * pa_attention_varlen_fp4 -- pa_attention_varlen over a 4-bit cache:
+ *   out[t][h][:] = sum_k softmax_k(scale * q[t][h] . K_k) V_k
+ * with K, V the cache's values, and everything else as there (positions, heads,
+ * block tables, bounds).  Slots of the last block past seq_lens[s] are never
+ * used, whatever they hold; a block id outside the pool is never dereferenced.
+ * dtype is that of q and out.  The host copies are optional; the kernels plan
+ * the step's work from the device arrays, so a captured call follows those.
+ * Supported: head_dim in {64, 128}; block_size 16; num_q_heads a multiple of
+ * num_kv_heads with at most 16 q-heads per kv-head; dtype f32 or bf16.
+ */
+int pa_attention_varlen_fp4(void* out, const void* q, const void* kv_cache, float k_scale,
+                            float v_scale, const int32_t* block_tables, int max_blocks_per_seq,
+                            const int32_t* seq_lens, const int32_t* query_start_loc,
+                            int num_seqs, int num_tokens, int max_query_len, int max_seq_len,
+                            int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                            int num_blocks, float scale, pa_dtype dtype, void* workspace,
+                            size_t workspace_bytes, const int32_t* seq_lens_host,
+                            const int32_t* query_start_loc_host, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -89,19 +89,6 @@ extern "C" int pa_reshape_and_cache(const void* k, const void* v, void* k_cache,
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-static bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-// A byte range [p, p + n) of caller memory (n = 0: empty, overlaps nothing).
-struct Range {
-  const void* p;
-  size_t n;
-  bool overlaps(const Range& o) const {
-    if (!p || !o.p || n == 0 || o.n == 0) return false;
-    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)o.p;
-    return a < b + o.n && b < a + n;
-  }
-};
-
 extern "C" int pa_plan_step(const int32_t* free_queue, int queue_len, int32_t* planner_state,
                             const int32_t* num_computed, const int32_t* query_lens,
                             int num_seqs, int32_t* block_tables, int max_blocks_per_seq,

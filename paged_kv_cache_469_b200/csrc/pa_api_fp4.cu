@@ -1,0 +1,234 @@
+// pa_api_fp4.cu -- the C ABI of the rotating append and of the 4-bit cache:
+// host-side argument checks and dispatch (declared in include/pa.h).
+#include <math.h>
+
+#include "pa.h"
+#include "pa_fp4.cuh"
+#include "pa_internal.cuh"
+
+using namespace pa;
+
+namespace {
+
+bool supported_dim(int d) { return d == 64 || d == 128; }
+bool positive(float x) { return x > 0.f && isfinite(x); }
+
+// [first row .. last row] of `heads` x `head_dim` elements, `stride` elements apart
+Range rows_range(const void* p, int rows, int64_t stride, int heads, int head_dim, int elem) {
+  return Range{p, rows > 0 ? ((size_t)(rows - 1) * stride + (size_t)heads * head_dim) * elem : 0};
+}
+
+int rope_append_impl(void* q_out, const void* q, int64_t q_stride, const void* k,
+                     int64_t k_stride, const void* v, int64_t v_stride, void* k_cache,
+                     void* v_cache, const int64_t* slot_mapping, const int64_t* positions,
+                     const float* cos_sin, int64_t max_position, int rotary_dim, int interleaved,
+                     int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                     int block_size, int num_blocks, pa_dtype dtype, bool fp4, float k_scale,
+                     float v_scale, struct CUstream_st* stream) {
+  if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads <= 0 || num_blocks < 0 ||
+      max_position < 0 || rotary_dim < 0 || rotary_dim > head_dim)
+    return PA_ERR_INVALID;
+  if (dtype != PA_DTYPE_F32 && dtype != PA_DTYPE_BF16) return PA_ERR_UNSUPPORTED;
+  if (block_size != kBlockSize || !supported_dim(head_dim)) return PA_ERR_UNSUPPORTED;
+  // a lane's two vectors are the two sides of eight rotation pairs; the 4-bit
+  // groups pair neighbouring lanes
+  if (rotary_dim % (fp4 && !interleaved ? 32 : 16) != 0) return PA_ERR_UNSUPPORTED;
+  if (fp4 && (!positive(k_scale) || !positive(v_scale) || !isfinite(6.f * k_scale) ||
+              !isfinite(6.f * v_scale)))
+    return PA_ERR_INVALID;
+  const int elem = dtype == PA_DTYPE_F32 ? 4 : 2;
+  const int64_t strides[3] = {q_stride, k_stride, v_stride};
+  for (int64_t s : strides)
+    if (s < 0 || s > INT64_MAX / 16 || s * elem % 16 != 0) return PA_ERR_INVALID;
+  if (num_tokens == 0) return PA_OK;
+  if (!k || !v || !k_cache || (!fp4 && !v_cache) || !slot_mapping) return PA_ERR_INVALID;
+  if (num_q_heads > 0 && (!q || !q_out)) return PA_ERR_INVALID;
+  if (rotary_dim > 0 && (!positions || !cos_sin)) return PA_ERR_INVALID;
+  const void* ptrs[7] = {q, q_out, k, v, k_cache, v_cache, cos_sin};
+  for (const void* p : ptrs)
+    if (!aligned_to(p, 16)) return PA_ERR_INVALID;
+  if (!aligned_to(slot_mapping, 8) || !aligned_to(positions, 8)) return PA_ERR_INVALID;
+  if (num_q_heads > 0) {
+    // in place, or apart from every input: rows are read and written by
+    // different warps in any order
+    const int64_t row = (int64_t)num_q_heads * head_dim;
+    const Range out = rows_range(q_out, num_tokens, row, num_q_heads, head_dim, elem);
+    const bool in_place = q_out == q && (q_stride == row || num_tokens == 1);
+    if ((!in_place && out.overlaps(rows_range(q, num_tokens, q_stride, num_q_heads, head_dim, elem))) ||
+        out.overlaps(rows_range(k, num_tokens, k_stride, num_kv_heads, head_dim, elem)) ||
+        out.overlaps(rows_range(v, num_tokens, v_stride, num_kv_heads, head_dim, elem)))
+      return PA_ERR_INVALID;
+  }
+  RopeAppendParams p{};
+  p.q_out = q_out;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.max_position = max_position;
+  p.rotary_dim = rotary_dim;
+  p.interleaved = interleaved != 0;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.num_blocks = num_blocks;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.k_six = 6.f * k_scale;
+  p.v_six = 6.f * v_scale;
+  return launch_rope_append(p, head_dim, dtype == PA_DTYPE_F32, fp4, (cudaStream_t)stream) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+// Workspace of attention over a 4-bit cache: the 256-byte header, the arrival
+// counters, and two partial results per CTA.
+struct Fp4Workspace {
+  size_t counters_off, ml_off, o_off, total;
+};
+Fp4Workspace fp4_workspace(int head_dim) {
+  Fp4Workspace w{};
+  w.counters_off = 256;
+  w.ml_off = w.counters_off + kFp4MaxCtas * sizeof(int);
+  w.o_off = w.ml_off + (size_t)kFp4MaxCtas * 2 * 16 * 2 * sizeof(float);
+  w.total = w.o_off + (size_t)kFp4MaxCtas * 2 * 16 * head_dim * sizeof(float);
+  return w;
+}
+
+}  // namespace
+
+extern "C" int pa_rope_append(void* q_out, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, void* k_cache,
+                              void* v_cache, const int64_t* slot_mapping,
+                              const int64_t* positions, const float* cos_sin,
+                              int64_t max_position, int rotary_dim, int interleaved,
+                              int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                              int block_size, int num_blocks, pa_dtype dtype,
+                              struct CUstream_st* stream) {
+  return rope_append_impl(q_out, q, q_stride, k, k_stride, v, v_stride, k_cache, v_cache,
+                          slot_mapping, positions, cos_sin, max_position, rotary_dim, interleaved,
+                          num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                          dtype, false, 1.f, 1.f, stream);
+}
+
+extern "C" int pa_rope_append_fp4(void* q_out, const void* q, int64_t q_stride, const void* k,
+                                  int64_t k_stride, const void* v, int64_t v_stride,
+                                  void* kv_cache, float k_scale, float v_scale,
+                                  const int64_t* slot_mapping, const int64_t* positions,
+                                  const float* cos_sin, int64_t max_position, int rotary_dim,
+                                  int interleaved, int num_tokens, int num_q_heads,
+                                  int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                  pa_dtype dtype, struct CUstream_st* stream) {
+  return rope_append_impl(q_out, q, q_stride, k, k_stride, v, v_stride, kv_cache, nullptr,
+                          slot_mapping, positions, cos_sin, max_position, rotary_dim, interleaved,
+                          num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                          dtype, true, k_scale, v_scale, stream);
+}
+
+extern "C" int pa_gather_fp4(void* k_out, void* v_out, const void* kv_cache, float k_scale,
+                             float v_scale, const int64_t* slots, int num_rows, int num_kv_heads,
+                             int head_dim, int block_size, int num_blocks, pa_dtype dtype,
+                             struct CUstream_st* stream) {
+  if (num_rows < 0 || num_kv_heads <= 0 || num_blocks < 0) return PA_ERR_INVALID;
+  if (dtype != PA_DTYPE_F32 && dtype != PA_DTYPE_BF16) return PA_ERR_UNSUPPORTED;
+  if (block_size != kBlockSize || !supported_dim(head_dim)) return PA_ERR_UNSUPPORTED;
+  if (!positive(k_scale) || !positive(v_scale)) return PA_ERR_INVALID;
+  if (num_rows == 0) return PA_OK;
+  if (!k_out || !v_out || !kv_cache || !slots) return PA_ERR_INVALID;
+  if (!aligned_to(k_out, 16) || !aligned_to(v_out, 16) || !aligned_to(kv_cache, 16) ||
+      !aligned_to(slots, 8))
+    return PA_ERR_INVALID;
+  const GatherFp4Params p{k_out,    v_out,        (const uint8_t*)kv_cache, slots,
+                          num_rows, num_kv_heads, num_blocks,               k_scale,
+                          v_scale};
+  return launch_gather_fp4(p, head_dim, dtype == PA_DTYPE_F32, (cudaStream_t)stream) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+extern "C" size_t pa_attention_fp4_workspace_size(int num_seqs, int num_tokens, int num_q_heads,
+                                                  int num_kv_heads, int head_dim) {
+  if (num_seqs < 0 || num_tokens < 0 || num_kv_heads <= 0 || num_q_heads <= 0) return 0;
+  if (num_q_heads % num_kv_heads != 0 || !supported_dim(head_dim)) return 0;
+  return fp4_workspace(head_dim).total;
+}
+
+extern "C" int pa_attention_varlen_fp4(
+    void* out, const void* q, const void* kv_cache, float k_scale, float v_scale,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+    const int32_t* query_start_loc, int num_seqs, int num_tokens, int max_query_len,
+    int max_seq_len, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+    int num_blocks, float scale, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+    const int32_t* seq_lens_host, const int32_t* query_start_loc_host,
+    struct CUstream_st* stream) {
+  if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0 || max_seq_len < 0 ||
+      num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks < 0 || max_blocks_per_seq < 0)
+    return PA_ERR_INVALID;
+  if (dtype != PA_DTYPE_F32 && dtype != PA_DTYPE_BF16) return PA_ERR_UNSUPPORTED;
+  if (block_size != kBlockSize || !supported_dim(head_dim)) return PA_ERR_UNSUPPORTED;
+  if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID;
+  const int group = num_q_heads / num_kv_heads;
+  if (group > kDecodeRows) return PA_ERR_UNSUPPORTED;
+  if (!positive(scale) || !positive(k_scale) || !positive(v_scale) || !positive(scale * k_scale))
+    return PA_ERR_INVALID;
+  if (max_query_len > max_seq_len) return PA_ERR_INVALID;
+  if ((long)max_blocks_per_seq * kBlockSize < (long)max_seq_len) return PA_ERR_INVALID;
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (!out || !q || !kv_cache || num_blocks == 0 || !block_tables || !seq_lens ||
+      !query_start_loc)
+    return PA_ERR_INVALID;
+  if (!aligned_to(out, 16) || !aligned_to(q, 16) || !aligned_to(kv_cache, 16) ||
+      !aligned_to(block_tables, 4) || !aligned_to(seq_lens, 4) || !aligned_to(query_start_loc, 4))
+    return PA_ERR_INVALID;
+  int rows = (int)min((long)max_query_len * group, (long)INT32_MAX);
+  if (seq_lens_host && query_start_loc_host) {
+    if (query_start_loc_host[0] != 0 || query_start_loc_host[num_seqs] != num_tokens)
+      return PA_ERR_INVALID;
+    int longest = 0;
+    for (int s = 0; s < num_seqs; ++s) {
+      const int ql = query_start_loc_host[s + 1] - query_start_loc_host[s];
+      const int L = seq_lens_host[s];
+      if (ql < 0 || ql > L || L > max_seq_len || ql > max_query_len) return PA_ERR_INVALID;
+      longest = max(longest, ql);
+    }
+    rows = longest * group;
+  }
+  const Fp4Workspace w = fp4_workspace(head_dim);
+  if (!workspace || workspace_bytes < w.total || !aligned_to(workspace, 16)) return PA_ERR_INVALID;
+  char* ws = (char*)workspace;
+  Fp4AttnParams p{};
+  p.out = out;
+  p.q = q;
+  p.kv_cache = (const uint8_t*)kv_cache;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.query_start_loc = query_start_loc;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_seq_len = max_seq_len;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = group;
+  p.num_blocks = num_blocks;
+  p.scale_log2 = scale * k_scale * 1.4426950408889634f;
+  p.v_scale = v_scale;
+  p.max_rows = INT32_MAX;
+  p.ws_status = (int*)ws;
+  p.ws_counters = (int*)(ws + w.counters_off);
+  p.ws_ml = (float*)(ws + w.ml_off);
+  p.ws_o = (float*)(ws + w.o_off);
+  return launch_decode_fp4(p, head_dim, dtype == PA_DTYPE_F32, rows, (cudaStream_t)stream) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}

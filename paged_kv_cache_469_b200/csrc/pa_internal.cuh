@@ -32,6 +32,19 @@ inline cudaError_t raise_smem_limit(Kernel kernel, int bytes, std::atomic<int> (
   return e;
 }
 
+inline bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// A byte range [p, p + n) of caller memory (n = 0: empty, overlaps nothing).
+struct Range {
+  const void* p;
+  size_t n;
+  bool overlaps(const Range& o) const {
+    if (!p || !o.p || n == 0 || o.n == 0) return false;
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)o.p;
+    return a < b + o.n && b < a + n;
+  }
+};
+
 // SMs of the current device (looked up once per device; 148 if the query fails)
 int device_sm_count();
 
@@ -145,6 +158,69 @@ cudaError_t launch_reshape_and_cache(const void* k, const void* v, void* k_cache
                                      const int64_t* slot_mapping, int num_tokens,
                                      int num_kv_heads, int head_dim, int num_blocks,
                                      int elem_bytes, cudaStream_t stream);
+
+// A step's new rows rotated and stored (pa_rope_append, pa_rope_append_fp4;
+// the latter's one cache is k_cache).
+struct RopeAppendParams {
+  void* q_out;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
+  void* k_cache;
+  void* v_cache;
+  const int64_t* slot_mapping;
+  const int64_t* positions;
+  const float* cos_sin;  // [max_position][rotary_dim]: cosines, then sines
+  int64_t max_position;
+  int rotary_dim;
+  int interleaved;
+  int num_tokens, num_q_heads, num_kv_heads, num_blocks;
+  float k_scale, v_scale, k_six, v_six;  // the tensors' scales, and 6 times them
+};
+cudaError_t launch_rope_append(const RopeAppendParams& p, int head_dim, bool f32, bool fp4,
+                               cudaStream_t stream);
+
+// Everything one launch of attention over a 4-bit cache reads.
+struct Fp4AttnParams {
+  void* out;
+  const void* q;
+  const uint8_t* kv_cache;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  int max_blocks_per_seq;
+  int max_seq_len;  // host bound: longer sequences are caller error and left unwritten
+  int num_seqs;
+  int num_tokens;
+  int num_q_heads;
+  int num_kv_heads;
+  int group;
+  int num_blocks;
+  float scale_log2;  // scale * k_scale * log2(e)
+  float v_scale;
+  int max_rows;      // decode kernel: sequences with more query rows per kv-head are not its own
+  int* ws_status;    // the workspace header
+  int* ws_counters;  // [kFp4MaxCtas]: arrivals at a unit that starts in that CTA, zero between calls
+  float* ws_ml;      // [kFp4MaxCtas][2][16][2] running max (log2 units) and sum
+  float* ws_o;       // [kFp4MaxCtas][2][16][D] unnormalised partial outputs
+};
+constexpr int kFp4MaxCtas = 256;
+// `rows`: most query rows per kv-head of a sequence the kernel takes.
+cudaError_t launch_decode_fp4(const Fp4AttnParams& p, int head_dim, bool f32, int rows,
+                              cudaStream_t stream);
+
+// Rows of a 4-bit cache as values (pa_gather_fp4).
+struct GatherFp4Params {
+  void* k_out;
+  void* v_out;
+  const uint8_t* kv_cache;
+  const int64_t* slots;
+  int num_rows, num_kv_heads, num_blocks;
+  float k_scale, v_scale;
+};
+cudaError_t launch_gather_fp4(const GatherFp4Params& p, int head_dim, bool f32,
+                              cudaStream_t stream);
 
 // CUDA-core kernel: every query row whose sequence has more than
 // min_rows_per_kv_head query rows per kv-head (0 = all rows).

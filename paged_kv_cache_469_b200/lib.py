@@ -22,7 +22,8 @@ PA_DTYPE_F32, PA_DTYPE_BF16 = 0, 1
 EXPORTS = ("pa_status_string", "pa_reshape_and_cache", "pa_attention_workspace_size",
            "pa_workspace_init", "pa_workspace_status", "pa_attention_varlen",
            "pa_attention_varlen_write_cache", "pa_attention_varlen_static_scratch",
-           "pa_plan_step")
+           "pa_plan_step", "pa_rope_append", "pa_rope_append_fp4", "pa_gather_fp4",
+           "pa_attention_fp4_workspace_size", "pa_attention_varlen_fp4")
 
 _lib = None
 
@@ -64,6 +65,25 @@ def library() -> ctypes.CDLL:
         lib.pa_plan_step.restype = c_int
         lib.pa_plan_step.argtypes = [c_p, c_int, c_p, c_p, c_p, c_int, c_p, c_int, c_int, c_p,
                                      c_p, c_p, c_int, c_p]
+        c_i64 = ctypes.c_int64
+        lib.pa_rope_append.restype = c_int
+        lib.pa_rope_append.argtypes = [c_p, c_p, c_i64, c_p, c_i64, c_p, c_i64, c_p, c_p, c_p,
+                                       c_p, c_p, c_i64, c_int, c_int, c_int, c_int, c_int, c_int,
+                                       c_int, c_int, c_int, c_p]
+        lib.pa_rope_append_fp4.restype = c_int
+        lib.pa_rope_append_fp4.argtypes = [c_p, c_p, c_i64, c_p, c_i64, c_p, c_i64, c_p, c_f, c_f,
+                                           c_p, c_p, c_p, c_i64, c_int, c_int, c_int, c_int,
+                                           c_int, c_int, c_int, c_int, c_int, c_p]
+        lib.pa_gather_fp4.restype = c_int
+        lib.pa_gather_fp4.argtypes = [c_p, c_p, c_p, c_f, c_f, c_p, c_int, c_int, c_int, c_int,
+                                      c_int, c_int, c_p]
+        lib.pa_attention_fp4_workspace_size.restype = c_sz
+        lib.pa_attention_fp4_workspace_size.argtypes = [c_int, c_int, c_int, c_int, c_int]
+        lib.pa_attention_varlen_fp4.restype = c_int
+        lib.pa_attention_varlen_fp4.argtypes = [c_p, c_p, c_p, c_f, c_f, c_p, c_int, c_p, c_p,
+                                                c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                                c_int, c_int, c_f, c_int, c_p, c_sz, c_p, c_p,
+                                                c_p]
         _lib = lib
     return _lib
 
@@ -240,3 +260,215 @@ def plan_step(free_queue: torch.Tensor, planner_state: torch.Tensor,
         _dev(slot_mapping, "slot_mapping"), slot_mapping.numel(), _stream(stream))
     if rc != PA_OK:
         raise PAError(rc, "pa_plan_step")
+
+
+def _on_device(name, fn, stream, tensors, *args):
+    """Call fn(*args, stream) with the tensors' device current.  ``tensors``: every
+    tensor of the call, by name; all must be CUDA tensors of one device."""
+    dev = tensors[0][1].get_device()
+    for what, t in tensors:
+        if t.get_device() != dev or dev < 0:
+            raise ValueError(f"{name}: {what} must be a CUDA tensor on the device of "
+                             f"{tensors[0][0]}")
+    if dev == torch.cuda.current_device():
+        s = stream.cuda_stream if stream is not None else \
+            torch._C._cuda_getCurrentRawStream(dev)
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(stream))
+    if rc != PA_OK:
+        raise PAError(rc, name)
+
+
+def _contiguous(*named) -> None:
+    for what, t in named:
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+
+
+def _rows(t: torch.Tensor, name: str, tokens: int, heads: int, d: int) -> int:
+    """Elements from one token's row to the next of a [tokens][heads][d] tensor
+    whose rows are contiguous (a slice of a fused projection, for instance)."""
+    st = t.stride()
+    if t.shape != (tokens, heads, d) or (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}] with contiguous rows")
+    return st[0] if tokens > 1 else heads * d
+
+
+def _rope_arguments(q, k, v, d, slot_mapping, positions, cos_sin, q_out):
+    """The arguments that both appends pass on alike, after their checks."""
+    t, hkv = k.shape[0], k.shape[1]
+    hq = q.shape[1]
+    if q.dtype != k.dtype or v.dtype != k.dtype or q_out.dtype != k.dtype:
+        raise TypeError("q, k, v and q_out must have one dtype")
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    if q_out.shape != (t, hq, d) or slot_mapping.shape != (t,):
+        raise ValueError("inconsistent sizes of q_out or slot_mapping")
+    rotary, longest, pos_ptr, cs_ptr = 0, 0, None, None
+    if cos_sin is not None:
+        if positions is None or positions.dtype != torch.int64:
+            raise TypeError("positions must be int64")
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+            raise TypeError("cos_sin must be a float32 [max_position, rotary_dim] tensor")
+        if positions.shape != (t,):
+            raise ValueError("inconsistent size of positions")
+        _contiguous(("positions", positions), ("cos_sin", cos_sin))
+        longest, rotary = cos_sin.shape
+        pos_ptr, cs_ptr = positions.data_ptr(), cos_sin.data_ptr()
+    _contiguous(("q_out", q_out), ("slot_mapping", slot_mapping))
+    head = (q_out.data_ptr(), q.data_ptr(), _rows(q, "q", t, hq, d), k.data_ptr(),
+            _rows(k, "k", t, hkv, d), v.data_ptr(), _rows(v, "v", t, hkv, d))
+    tail = (slot_mapping.data_ptr(), pos_ptr, cs_ptr, longest, rotary)
+    tensors = [("k", k), ("q", q), ("v", v), ("q_out", q_out), ("slot_mapping", slot_mapping)]
+    if cos_sin is not None:
+        tensors += [("positions", positions), ("cos_sin", cos_sin)]
+    return head, tail, tensors, t, hq, hkv
+
+
+def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                positions: torch.Tensor | None, cos_sin: torch.Tensor | None, *,
+                q_out: torch.Tensor | None = None, interleaved: bool = False,
+                stream=None) -> torch.Tensor:
+    """Queries and keys rotated to their positions, keys and values stored in their
+    slots, in one launch (see pa_rope_append in pa.h).
+
+    q: [T, Hq, D], k, v: [T, Hkv, D], each row contiguous (slices of a fused
+    projection are fine); caches: [num_blocks, Hkv, 16, D]; slot_mapping,
+    positions: int64 [T]; cos_sin: float32 [max_position, rotary_dim], the
+    cosines and then the sines of a position's angles (None: nothing is
+    rotated).  Returns q_out (a new tensor unless given)."""
+    num_blocks, hkv, bs, d = k_cache.shape
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    head, tail, tensors, t, hq, heads = _rope_arguments(q, k, v, d, slot_mapping, positions,
+                                                        cos_sin, q_out)
+    if heads != hkv or v_cache.shape != k_cache.shape:
+        raise ValueError("rope_append: the caches' shapes do not fit k and v")
+    if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
+        raise TypeError("the caches must have the dtype of k")
+    _contiguous(("k_cache", k_cache), ("v_cache", v_cache))
+    _on_device("pa_rope_append", library().pa_rope_append, stream,
+               tensors + [("k_cache", k_cache), ("v_cache", v_cache)], *head,
+               k_cache.data_ptr(), v_cache.data_ptr(), *tail, int(interleaved), t, hq, hkv, d,
+               bs, num_blocks, _dtype_code(k))
+    return q_out
+
+
+FP4_BLOCK_SIZE = 16  # tokens of a block, and so of a tile
+
+
+def new_fp4_cache(num_blocks: int, num_kv_heads: int, head_dim: int,
+                  device="cuda") -> torch.Tensor:
+    """A zeroed 4-bit cache: uint8 [num_blocks, num_kv_heads, 18 * head_dim], K and
+    V of 16 tokens of one kv-head per tile (the layout is in pa.h)."""
+    return torch.zeros(num_blocks, num_kv_heads, 18 * head_dim, dtype=torch.uint8, device=device)
+
+
+def _fp4_cache(kv_cache: torch.Tensor):
+    num_blocks, hkv, tile = kv_cache.shape
+    if kv_cache.dtype != torch.uint8 or tile % 18:
+        raise TypeError("kv_cache must be uint8 [num_blocks, num_kv_heads, 18 * head_dim]")
+    _contiguous(("kv_cache", kv_cache))
+    return num_blocks, hkv, tile // 18
+
+
+def rope_append_fp4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_cache: torch.Tensor,
+                    slot_mapping: torch.Tensor, positions: torch.Tensor | None,
+                    cos_sin: torch.Tensor | None, *, k_scale: float = 1.0, v_scale: float = 1.0,
+                    q_out: torch.Tensor | None = None, interleaved: bool = False,
+                    stream=None) -> torch.Tensor:
+    """``rope_append`` into a 4-bit cache (see pa_rope_append_fp4 in pa.h); k_scale and
+    v_scale are the tensors' own scales."""
+    num_blocks, hkv, d = _fp4_cache(kv_cache)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    head, tail, tensors, t, hq, heads = _rope_arguments(q, k, v, d, slot_mapping, positions,
+                                                        cos_sin, q_out)
+    if heads != hkv:
+        raise ValueError("rope_append_fp4: the cache's shape does not fit k and v")
+    _on_device("pa_rope_append_fp4", library().pa_rope_append_fp4, stream,
+               tensors + [("kv_cache", kv_cache)], *head, kv_cache.data_ptr(), float(k_scale),
+               float(v_scale), *tail, int(interleaved), t, hq, hkv, d, FP4_BLOCK_SIZE,
+               num_blocks, _dtype_code(k))
+    return q_out
+
+
+def gather_fp4(kv_cache: torch.Tensor, slots: torch.Tensor, *, k_scale: float = 1.0,
+               v_scale: float = 1.0, dtype=torch.bfloat16, k_out: torch.Tensor | None = None,
+               v_out: torch.Tensor | None = None, stream=None):
+    """K and V values ([n, Hkv, D] each) of the slots (int64 [n]) of a 4-bit cache; rows
+    of slots outside the pool are left as they are (see pa_gather_fp4 in pa.h)."""
+    num_blocks, hkv, d = _fp4_cache(kv_cache)
+    n = slots.shape[0]
+    if slots.dtype != torch.int64:
+        raise TypeError("slots must be int64")
+    if k_out is None:
+        k_out = torch.zeros(n, hkv, d, dtype=dtype, device=kv_cache.device)
+    if v_out is None:
+        v_out = torch.zeros(n, hkv, d, dtype=k_out.dtype, device=kv_cache.device)
+    if k_out.shape != (n, hkv, d) or v_out.shape != (n, hkv, d):
+        raise ValueError("gather_fp4: k_out and v_out must be [n, num_kv_heads, head_dim]")
+    if v_out.dtype != k_out.dtype:
+        raise TypeError("k_out and v_out must have one dtype")
+    _contiguous(("slots", slots), ("k_out", k_out), ("v_out", v_out))
+    _on_device("pa_gather_fp4", library().pa_gather_fp4, stream,
+               [("kv_cache", kv_cache), ("slots", slots), ("k_out", k_out), ("v_out", v_out)],
+               k_out.data_ptr(), v_out.data_ptr(), kv_cache.data_ptr(), float(k_scale),
+               float(v_scale), slots.data_ptr(), n, hkv, d, FP4_BLOCK_SIZE, num_blocks,
+               _dtype_code(k_out))
+    return k_out, v_out
+
+
+def new_fp4_workspace(num_seqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
+                      head_dim: int, device="cuda", stream=None) -> torch.Tensor:
+    """A zeroed workspace of ``attention_varlen_fp4`` for steps up to these sizes."""
+    n = int(library().pa_attention_fp4_workspace_size(num_seqs, num_tokens, num_q_heads,
+                                                      num_kv_heads, head_dim))
+    if n == 0:
+        raise ValueError("invalid workspace bounds")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    _on_device("pa_workspace_init", library().pa_workspace_init, stream, [("workspace", ws)],
+               ws.data_ptr(), n)
+    return ws
+
+
+def attention_varlen_fp4(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor,
+                         block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                         query_start_loc: torch.Tensor, *, max_query_len: int, max_seq_len: int,
+                         scale: float, workspace: torch.Tensor, k_scale: float = 1.0,
+                         v_scale: float = 1.0, seq_lens_host=None, query_start_loc_host=None,
+                         stream=None) -> torch.Tensor:
+    """Paged attention of one flattened step over a 4-bit cache (see
+    pa_attention_varlen_fp4 in pa.h)."""
+    num_blocks, hkv, d = _fp4_cache(kv_cache)
+    t, hq, qd = q.shape
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or \
+            query_start_loc.dtype != torch.int32:
+        raise TypeError("block_tables, seq_lens and query_start_loc must be int32")
+    if out.dtype != q.dtype:
+        raise TypeError("out must have the dtype of q")
+    s = seq_lens.shape[0]
+    if qd != d or out.shape != q.shape or block_tables.shape[0] != s or \
+            query_start_loc.shape[0] != s + 1:
+        raise ValueError("attention_varlen_fp4: inconsistent sizes")
+    _contiguous(("out", out), ("q", q), ("block_tables", block_tables), ("seq_lens", seq_lens),
+                ("query_start_loc", query_start_loc), ("workspace", workspace))
+    sl_ptr, sl_keep = _host_i32(seq_lens_host)
+    qs_ptr, qs_keep = _host_i32(query_start_loc_host)
+    if (sl_ptr and sl_keep.shape != (s,)) or (qs_ptr and qs_keep.shape != (s + 1,)):
+        raise ValueError("attention_varlen_fp4: the host copies' sizes do not fit")
+    _on_device("pa_attention_varlen_fp4", library().pa_attention_varlen_fp4, stream,
+               [("q", q), ("out", out), ("kv_cache", kv_cache), ("block_tables", block_tables),
+                ("seq_lens", seq_lens), ("query_start_loc", query_start_loc),
+                ("workspace", workspace)],
+               out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), float(k_scale),
+               float(v_scale), block_tables.data_ptr(), block_tables.shape[1],
+               seq_lens.data_ptr(), query_start_loc.data_ptr(), s, t, max_query_len,
+               max_seq_len, hq, hkv, d, FP4_BLOCK_SIZE, num_blocks, float(scale),
+               _dtype_code(q), workspace.data_ptr(),
+               workspace.numel() * workspace.element_size(), sl_ptr, qs_ptr)
+    del sl_keep, qs_keep
+    return out

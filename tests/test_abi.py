@@ -177,3 +177,94 @@ def test_missing_library_fails_loudly(monkeypatch, tmp_path):
     monkeypatch.setattr(palib, "LIB_PATH", str(tmp_path / "nope.so"))
     with pytest.raises(RuntimeError, match="missing"):
         palib.library()
+
+
+def _rope(L, fp4=False, **kw):
+    args = dict(qo=1 << 20, q=2 << 20, qs=512, k=3 << 20, ks=128, v=4 << 20, vs=128, kc=5 << 20,
+                vc=6 << 20, gk=1.0, gv=1.0, slots=16, pos=16, cs=16, mp=100, r=64, il=0, T=4, hq=8,
+                hkv=2, d=64, bs=16, nb=4, dt=1, stream=None)
+    args.update(kw)
+    drop = ("vc",) if fp4 else ("gk", "gv")
+    f = L.pa_rope_append_fp4 if fp4 else L.pa_rope_append
+    return f(*(v for k, v in args.items() if k not in drop))
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_rope_append_argument_checks(L, fp4):
+    def c(**kw):
+        return _rope(L, fp4, **kw)
+    assert c(d=96) == palib.PA_ERR_UNSUPPORTED
+    assert c(bs=32) == palib.PA_ERR_UNSUPPORTED
+    assert c(dt=2) == palib.PA_ERR_UNSUPPORTED
+    assert c(r=40) == palib.PA_ERR_UNSUPPORTED
+    assert c(r=80) == palib.PA_ERR_INVALID          # more than head_dim
+    assert c(r=-16) == palib.PA_ERR_INVALID
+    assert c(T=-1) == palib.PA_ERR_INVALID
+    assert c(hkv=0) == palib.PA_ERR_INVALID
+    assert c(nb=-1) == palib.PA_ERR_INVALID
+    assert c(mp=-1) == palib.PA_ERR_INVALID
+    assert c(T=0) == palib.PA_OK                    # nothing to do, nothing launched
+    for name in ("qo", "q", "k", "v", "kc", "slots", "pos", "cs"):
+        assert c(**{name: 0}) == palib.PA_ERR_INVALID, name
+        assert c(**{name: 20}) == palib.PA_ERR_INVALID, name  # misaligned
+    assert c(ks=-128) == palib.PA_ERR_INVALID
+    assert c(qs=516) == palib.PA_ERR_INVALID        # rows not 16-byte aligned
+    assert c(qo=2 << 20, qs=1024) == palib.PA_ERR_INVALID   # "in place", but with gaps
+    assert c(qo=(2 << 20) + 1024) == palib.PA_ERR_INVALID   # overlapping q
+    assert c(qo=3 << 20) == palib.PA_ERR_INVALID            # overlapping k
+    assert c(qo=(4 << 20) - 16) == palib.PA_ERR_INVALID     # overlapping v
+    if fp4:
+        assert c(r=48) == palib.PA_ERR_UNSUPPORTED          # halves: groups of 16 in pairs
+        for bad in (0.0, -1.0, float("nan"), float("inf"), 3e38):
+            assert c(gk=bad) == palib.PA_ERR_INVALID
+            assert c(gv=bad) == palib.PA_ERR_INVALID
+    else:
+        assert c(vc=0) == palib.PA_ERR_INVALID
+
+
+def test_gather_fp4_argument_checks(L):
+    def c(**kw):
+        args = dict(ko=16, vo=16, kv=16, gk=1.0, gv=1.0, slots=16, n=3, hkv=2, d=64, bs=16, nb=4,
+                    dt=1, stream=None)
+        args.update(kw)
+        return L.pa_gather_fp4(*args.values())
+    assert c(d=32) == palib.PA_ERR_UNSUPPORTED
+    assert c(bs=8) == palib.PA_ERR_UNSUPPORTED
+    assert c(dt=3) == palib.PA_ERR_UNSUPPORTED
+    assert c(n=-1) == palib.PA_ERR_INVALID
+    assert c(gk=0.0) == palib.PA_ERR_INVALID
+    assert c(ko=0) == palib.PA_ERR_INVALID
+    assert c(kv=8) == palib.PA_ERR_INVALID
+    assert c(slots=4) == palib.PA_ERR_INVALID
+    assert c(n=0) == palib.PA_OK
+
+
+def _fp4(L, **kw):
+    args = dict(out=16, q=16, kv=16, gk=1.0, gv=1.0, bt=16, mb=8, sl=16, qsl=16, S=1, T=1, mq=1,
+                ms=16, hq=8, hkv=2, d=64, bs=16, nb=4, scale=0.125, dt=1, ws=0, wsb=0, slh=None,
+                qslh=None, stream=None)
+    args.update(kw)
+    return L.pa_attention_varlen_fp4(*args.values())
+
+
+def test_fp4_attention_argument_checks(L):
+    assert L.pa_attention_fp4_workspace_size(4, 8, 8, 2, 64) > 0
+    assert L.pa_attention_fp4_workspace_size(4, 8, 8, 3, 64) == 0
+    assert L.pa_attention_fp4_workspace_size(-1, 8, 8, 2, 64) == 0
+    assert _fp4(L, d=96) == palib.PA_ERR_UNSUPPORTED
+    assert _fp4(L, bs=32) == palib.PA_ERR_UNSUPPORTED
+    assert _fp4(L, dt=7) == palib.PA_ERR_UNSUPPORTED
+    assert _fp4(L, hkv=3) == palib.PA_ERR_INVALID
+    assert _fp4(L, hq=64, hkv=2) == palib.PA_ERR_UNSUPPORTED
+    for bad in (0.0, -1.0, float("nan"), float("inf")):
+        assert _fp4(L, scale=bad) == palib.PA_ERR_INVALID
+        assert _fp4(L, gk=bad) == palib.PA_ERR_INVALID
+        assert _fp4(L, gv=bad) == palib.PA_ERR_INVALID
+    assert _fp4(L, mq=20, ms=16) == palib.PA_ERR_INVALID
+    assert _fp4(L, mb=0) == palib.PA_ERR_INVALID
+    assert _fp4(L, nb=0) == palib.PA_ERR_INVALID
+    assert _fp4(L, q=8) == palib.PA_ERR_INVALID
+    assert _fp4(L, kv=0) == palib.PA_ERR_INVALID
+    assert _fp4(L, S=-1) == palib.PA_ERR_INVALID
+    assert _fp4(L, T=0) == palib.PA_OK
+    assert _fp4(L) == palib.PA_ERR_INVALID          # no workspace

@@ -1,0 +1,239 @@
+"""pa_attention_varlen_fp4 against fp64 attention over the cache's exact values."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_469_b200 import lib
+from tests import fp4_side
+
+pytestmark = pytest.mark.gpu
+
+
+class Step:
+    """A step over a random 4-bit pool.  ``junk``: slots that hold no token get
+    all-one bytes (NaN scales)."""
+
+    def __init__(self, seed, lens, qls, hq, hkv, d, dtype="bf16", spread=1.0, q_spread=1.0,
+                 junk=True, extra_tokens=0):
+        rng = np.random.default_rng(seed)
+        lens, qls = np.asarray(lens, np.int32), np.asarray(qls, np.int32)
+        held = -(-lens // 16)
+        blocks = int(held.sum()) + 4
+        order = rng.permutation(blocks).astype(np.int32)
+        wide = max(1, int(held.max()))
+        self.tables = np.full((len(lens), wide), -5, np.int32)
+        pool = fp4_side.random_tiles(rng, blocks * hkv, d, spread).reshape(blocks, hkv, 18 * d)
+        at = 0
+        for s, n in enumerate(held):
+            self.tables[s, :n] = order[at:at + n]
+            at += n
+            if junk and lens[s] % 16:
+                for off in range(lens[s] % 16, 16):
+                    for h in range(hkv):
+                        fp4_side.put_row(pool[self.tables[s, n - 1], h], off, d, [15] * d,
+                                         [255] * (d // 16), [15] * d, [255] * (d // 16))
+        if junk:
+            pool[order[at:]] = 255
+        self.lens, self.pool = lens, pool
+        self.qsl = np.concatenate([[0], np.cumsum(qls)]).astype(np.int32)
+        t = int(self.qsl[-1]) + extra_tokens
+        dt = torch.float32 if dtype == "f32" else torch.bfloat16
+        q = torch.from_numpy((rng.standard_normal((t, hq, d)) * q_spread).astype(np.float32)).to(dt)
+        self.q64 = q.double().numpy()
+        self.q, self.cache = q.cuda(), torch.from_numpy(pool).cuda()
+        self.dev = [torch.from_numpy(x).cuda() for x in (self.tables, self.lens, self.qsl)]
+        self.scale = d ** -0.5
+        self.k_scale, self.v_scale = 0.8, 1.7
+        self.max_q, self.max_len = int(max(1, qls.max())), int(max(1, lens.max()))
+        self.ws = lib.new_fp4_workspace(len(lens), t, hq, hkv, d)
+        self.dtype = dtype
+
+    def run(self, host=False, out=None, **kw):
+        if out is None:
+            out = torch.full_like(self.q, float("nan"))
+        args = dict(max_query_len=self.max_q, max_seq_len=self.max_len, scale=self.scale,
+                    workspace=self.ws, k_scale=self.k_scale, v_scale=self.v_scale,
+                    seq_lens_host=self.lens if host else None,
+                    query_start_loc_host=self.qsl if host else None)
+        return lib.attention_varlen_fp4(out, self.q, self.cache, *self.dev, **{**args, **kw})
+
+    def check(self, out):
+        rows = int(self.qsl[-1])
+        want, mass, reach = fp4_side.attention(self.q64[:rows], self.pool, self.tables, self.lens,
+                                               self.qsl, self.scale, self.k_scale, self.v_scale)
+        got = out[:rows].double().cpu().numpy()
+        d, n = want.shape[-1], float(self.lens.max())
+        half = 2.0 ** -8 if self.dtype == "bf16" else 2.0 ** -24
+        # a probability: rounded to f16 (two of them for fp32), its exponential
+        # and the sums of up to n terms in fp32 (blocked: far fewer in a row
+        # than n; sqrt(n) covers them), its score's error: up to D products and
+        # sums of fp32 and the split query
+        score = (d + 8) * 2.0 ** -24 * (1 + reach)
+        p_half = 2.0 ** -11 if self.dtype == "bf16" else 2.0 ** -21
+        rel = p_half + 2.0 ** -20 + np.sqrt(n) * 2.0 ** -23 + 2 * score
+        vmax = 2 * np.abs(fp4_side.E2M1).max() * 8 * self.v_scale
+        bound = half * np.abs(want) + rel[..., None] * 1.01 * mass + n * 2.0 ** -32 * vmax
+        worst = np.max(np.abs(got - want) / bound) if want.size else 0.0
+        assert np.isfinite(got).all() and worst <= 1.0, f"{worst:.3f} of the bound"
+        head = self.ws[:256 + 1024].cpu()
+        assert not head.any(), "the workspace header and counters are zero between calls"
+        return worst
+
+
+SHAPES = [(32, 8, 128), (32, 4, 64), (4, 4, 64), (8, 1, 128), (16, 1, 128), (16, 1, 64),
+          (6, 2, 64), (7, 1, 128)]
+
+
+@pytest.mark.parametrize("hq,hkv,d", SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_steps(hq, hkv, d, dtype):
+    st = Step(d + hq, [1, 2, 15, 16, 17, 31, 33, 100, 517, 1203], [1] * 10, hq, hkv, d, dtype)
+    a = st.run()
+    st.check(a)
+    assert torch.equal(a, st.run(host=True)) and torch.equal(a, st.run())
+
+
+@pytest.mark.parametrize("hq,hkv,d", SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_several_query_tokens(hq, hkv, d, dtype):
+    st = Step(2 * d + hq, [1, 5, 16, 40, 3, 300, 0, 129, 64], [1, 5, 2, 9, 0, 7, 0, 16, 3], hq, hkv,
+              d, dtype)
+    a = st.run()
+    st.check(a)
+    assert torch.equal(a, st.run(host=True))
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (32, 4, 64), (3, 1, 128), (8, 1, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,qls", [([130], [130]), ([700, 65, 1], [257, 65, 1]),
+                                      ([400, 20, 999, 300], [128, 1, 200, 129])])
+def test_prompt_chunks(hq, hkv, d, dtype, lens, qls):
+    st = Step(sum(lens) + d, lens, qls, hq, hkv, d, dtype)
+    a = st.run()
+    st.check(a)
+    st.check(st.run(host=True))
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (8, 1, 64), (16, 1, 128)])
+@pytest.mark.parametrize("lens", [[20011], [9000, 3, 12000], [16 * 148 * 16], [16 * 148 * 16 + 1]])
+def test_long_contexts_over_many_processors(hq, hkv, d, lens):
+    st = Step(lens[0] + d, lens, [1] * len(lens), hq, hkv, d, junk=False)
+    a = st.run()
+    st.check(a)
+    for _ in range(3):
+        assert torch.equal(a, st.run())
+
+
+def test_many_sequences():
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 60, 1300)
+    st = Step(11, lens, (lens > 0) * rng.integers(0, 2, 1300), 4, 2, 64, junk=False)
+    st.check(st.run())
+
+
+@pytest.mark.parametrize("spread,q_spread", [(30.0, 4.0), (1e-4, 1e-4), (1.0, 1e20), (1.0, 1e-30)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_extreme_scores(spread, q_spread, dtype):
+    """Peaked rows, flat rows, and queries far from 1 (with a scale that undoes it)."""
+    st = Step(5, [700, 90, 1000], [1, 70, 2], 8, 2, 128, dtype, spread, q_spread)
+    if q_spread > 100 or q_spread < 1e-10:
+        st.scale = st.scale / q_spread
+    st.check(st.run())
+
+
+def test_rows_behind_the_last_sequence_stay():
+    st = Step(8, [50, 200, 33], [1, 100, 2], 8, 2, 64, extra_tokens=9)
+    out = torch.full_like(st.q, 5.0)
+    st.run(out=out)
+    st.check(out)
+    assert (out[int(st.qsl[-1]):] == 5.0).all()
+
+
+def test_stream_and_graph_follow_the_device_lengths():
+    st = Step(9, [600, 1500, 40], [1, 1, 1], 8, 2, 128, junk=False)
+    want = st.run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = st.run(stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(want, got)
+    out = torch.empty_like(st.q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        st.run(out=out)
+    g.replay()
+    assert torch.equal(out, want)
+    st.lens = np.array([77, 900, 33], np.int32)
+    st.dev[1].copy_(torch.from_numpy(st.lens))
+    g.replay()
+    st.check(out)
+
+
+def test_append_then_attend_as_a_decode_loop():
+    """Prompt chunk and decodes: rotate and append, then attend, step by step; the
+    queries that the append rotated, the rows that it stored."""
+    from tests.test_rope_append_gpu import table
+    hq, hkv, d, steps = 8, 2, 64, 4
+    rng = np.random.default_rng(21)
+    cs_host = table(2000, d)
+    cs = torch.from_numpy(cs_host).cuda()
+    lens = np.array([37, 0, 200], np.int32)
+    blocks = 60
+    tables = rng.permutation(blocks).reshape(3, 20).astype(np.int32)
+    cache = lib.new_fp4_cache(blocks, hkv, d)
+    rows = {s: [] for s in range(3)}  # (codes and scales) of each stored token
+    ws = lib.new_fp4_workspace(3, 400, hq, hkv, d)
+    for step in range(steps + 1):
+        ql = lens + np.array([0, 90, 0], np.int32) if step == 0 else np.ones(3, np.int32)
+        before = np.zeros(3, np.int32) if step == 0 else lens
+        lens = before + ql
+        t = int(ql.sum())
+        pos = np.concatenate([np.arange(b, b + n) for b, n in zip(before, ql)])
+        seq = np.repeat(np.arange(3), ql)
+        slots = tables[seq, pos // 16] * 16 + pos % 16
+        qkv = torch.from_numpy(rng.standard_normal((t, hq + 2 * hkv, d)).astype(np.float32))
+        q, k, v = qkv.bfloat16().cuda().split([hq, hkv, hkv], 1)
+        q_rot = lib.rope_append_fp4(q, k, v, cache, torch.from_numpy(slots).long().cuda(),
+                                    torch.from_numpy(pos).long().cuda(), cs, k_scale=0.5)
+        qsl = np.concatenate([[0], np.cumsum(ql)]).astype(np.int32)
+        out = torch.empty_like(q_rot)
+        lib.attention_varlen_fp4(out, q_rot, cache, *(torch.from_numpy(x).cuda() for x in
+                                                      (tables, lens, qsl)),
+                                 max_query_len=int(ql.max()), max_seq_len=320, scale=d ** -0.5,
+                                 workspace=ws, k_scale=0.5)
+        kc, ks = fp4_side.quantise(fp4_side.rotate_f32(k.float().cpu().numpy(), cs_host, pos,
+                                                       False), 0.5)
+        vc, vs = fp4_side.quantise(v.float().cpu().numpy(), 1.0)
+        pool = cache.cpu().numpy()
+        for i in range(t):
+            rows[seq[i]].append((kc[i], ks[i], vc[i], vs[i]))
+        want_pool = np.zeros_like(pool)
+        for s in range(3):
+            for p_, r in enumerate(rows[s]):
+                for h in range(hkv):
+                    fp4_side.put_row(want_pool[tables[s, p_ // 16], h], p_ % 16, d, r[0][h],
+                                     r[1][h], r[2][h], r[3][h])
+        assert np.array_equal(pool, want_pool)
+        st = Step.__new__(Step)
+        st.qsl, st.q64, st.pool, st.tables, st.lens = qsl, q_rot.double().cpu().numpy(), pool, tables, lens
+        st.scale, st.k_scale, st.v_scale, st.dtype, st.ws = d ** -0.5, 0.5, 1.0, "bf16", ws
+        st.check(out)
+
+
+def test_binding_refusals():
+    st = Step(1, [20], [1], 8, 2, 64)
+    with pytest.raises(TypeError):
+        lib.attention_varlen_fp4(st.q, st.q, st.cache, st.dev[0].long(), *st.dev[1:],
+                                 max_query_len=1, max_seq_len=20, scale=1.0, workspace=st.ws)
+    with pytest.raises(ValueError):
+        st.run(seq_lens_host=np.array([1, 2], np.int32), query_start_loc_host=st.qsl)
+    for bad in (dict(scale=0.0), dict(k_scale=-1.0), dict(v_scale=float("inf")),
+                dict(max_seq_len=1000), dict(max_query_len=30), dict(workspace=st.ws[:512]),
+                dict(seq_lens_host=np.array([21], np.int32), query_start_loc_host=st.qsl)):
+        with pytest.raises(lib.PAError):
+            st.run(**bad)
+    st.cache = st.cache[..., :1000].contiguous()
+    with pytest.raises(TypeError):
+        st.run()
