@@ -41,19 +41,17 @@ namespace {
 
 constexpr float kRescale = 8.f;   // log2 units: the running max moves only past 2^8
 constexpr float kPShift = 7.f;    // P is held times 2^7
-constexpr int kMaxWarps = 16;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -64,10 +62,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-// code pair in byte I of w, as f16, times s
-template <int I>
-__device__ __forceinline__ uint32_t deq(uint32_t w, __half2 s) {
-  return bits(__hmul2(e2m1x2_to_half2(w >> (8 * I) & 255u), s));
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
+// the eight codes of a word as f16 pairs, times s
+__device__ __forceinline__ void deq8(uint32_t w, __half2 s, uint32_t (&d)[4]) {
+  __half2 x[4];
+  e2m1x8_to_half2(w, x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = bits(__hmul2(x[i], s));
 }
 
 // shape of one kernel
@@ -75,84 +77,69 @@ template <int D_, int NT_, int QP_>
 struct Shape {
   static constexpr int D = D_, NT = NT_, QP = QP_;
   static constexpr int R = 8 * NT;                 // query rows of a unit
-  static constexpr bool kSmall = D * NT * QP <= 128;  // fits 128 registers a thread
-  static constexpr int kWarps = kSmall ? 16 : 8;
+  static constexpr int kWarps = D * NT * QP <= 64 ? 16 : D * NT * QP <= 128 ? 12 : 8;
   static constexpr int kTile = Fp4Tile<D>::bytes;
-  static constexpr int kStages = (kSmall ? 4 : 8) * (128 / D);
-  static constexpr int kRing = kStages * kTile;    // one warp's ring
   static constexpr int kPart = R * D * 4;          // one partial O
+  // stages of one warp's ring, two tiles each: what the shared memory beside
+  // the parts holds
+  static constexpr int kStages = (211 * 1024 / kWarps - kPart) / (2 * kTile);
+  static constexpr int kRing = kStages * 2 * kTile;
   static constexpr int kSteps = D / 16;            // MMA k-steps of S, M-tiles of O
   static constexpr int kChunkK = D / 4;            // dims of a lane's K chunk
   static constexpr int ring_off = 0;
   static constexpr int part_off = ring_off + kWarps * kRing;  // first parts
   static constexpr int total = part_off + kWarps * kPart;
-  static_assert(kRing >= kPart, "a warp's last part takes its ring's place");
-  static_assert(total <= 220 * 1024, "shared memory of one CTA");
+  // Units up to this many blocks are not cut between CTAs: a cut costs the
+  // joining CTA two more round trips to memory (some 3 us), the stretches'
+  // unequal lengths at most this many blocks over the warps of a CTA
+  static constexpr int kWhole = 8 * kWarps;
+  static_assert(kStages >= 3 && kRing >= kPart, "a warp's last part takes its ring's place");
 };
 
 // where a part of a unit belongs
 struct PartMeta {
-  long long unit_start;  // of the unit, on the line of blocks
-  int nblk;
-  int seq, head, rg;     // row group
-  int valid, ended;      // holds a part; the part reaches the unit's end
-};
-
-template <typename S>
-struct Shared {
-  unsigned long long bars[S::kWarps * S::kStages];
-  PartMeta meta[S::kWarps][2];
-  float ml[S::kWarps][2][S::R][2];
-  long long scan[kMaxWarps + 1];
-  long long start_pre[kMaxWarps];
-  int start_seq[kMaxWarps];
-  int abort;
-  int last[2];
+  int unit_start, nblk;       // of the unit, on the line of blocks
+  int q0, head, row0, nrows;  // the unit's first query row of the kv-head, and its rows
+  int valid, ended;           // holds a part; the part reaches the unit's end
 };
 
 // a sequence as the kernel sees it: its units' blocks on the line
 struct Seq {
   int q0, ql, L, nblk, rgs;
 };
+template <typename S>
+struct Shared {
+  unsigned long long bars[S::kWarps * S::kStages];
+  PartMeta meta[S::kWarps][2];
+  float ml[S::kWarps][2][S::R][2];
+  // of the sequences under way: q0, ql, L (as read), and their blocks on the
+  // line summed over the warp that read them
+  int4 seqs[S::kWarps * 32];
+  int abort;
+  int last[2];
+};
+
+template <int R>
+__device__ __forceinline__ Seq make_seq(const Fp4AttnParams& p, int q0, int ql, int L) {
+  const bool mine = ql > 0 && ql <= L && L <= p.max_seq_len && ql <= p.max_q;
+  return Seq{q0, ql, L, mine ? (L + kBlockSize - 1) / kBlockSize : 0,
+             mine ? (ql * p.group + R - 1) / R : 0};
+}
 template <int R>
 __device__ __forceinline__ Seq load_seq(const Fp4AttnParams& p, int s) {
-  Seq r;
-  r.q0 = p.query_start_loc[s];
-  r.ql = p.query_start_loc[s + 1] - r.q0;
-  r.L = p.seq_lens[s];
-  const long long rows = (long long)r.ql * p.group;
-  const bool mine = r.ql > 0 && r.ql <= r.L && r.L <= p.max_seq_len && rows <= p.max_rows;
-  r.nblk = mine ? (r.L + kBlockSize - 1) / kBlockSize : 0;
-  r.rgs = mine ? (int)((rows + R - 1) / R) : 0;
-  return r;
-}
-template <int R>
-__device__ __forceinline__ long long seq_cost(const Fp4AttnParams& p, int s) {
-  const Seq q = load_seq<R>(p, s);
-  return (long long)q.nblk * q.rgs * p.num_kv_heads;
+  const int q0 = p.query_start_loc[s];
+  return make_seq<R>(p, q0, p.query_start_loc[s + 1] - q0, p.seq_lens[s]);
 }
 
-// inclusive block-wide sum of one value per thread; *total gets the whole sum
-template <int kWarps>
-__device__ __forceinline__ long long block_scan(long long x, long long* sh, long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) sh[warp] = x;
-  __syncthreads();
-  long long before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const long long y = sh[w];
-    if (w < warp) before += y;
-    all += y;
-  }
-  *total = all;
-  return x + before;
+// a / b for 0 <= a, 0 < b: from the quotient in fp32, off by one at most below
+// 2^22, where its error is under 2^22 * 2^-22
+__device__ __forceinline__ int divide(int a, int b) {
+  if (a >= 1 << 22) return a / b;
+  int q = (int)__fdividef((float)a, (float)b);
+  const int r = a - q * b;
+  if (r < 0) --q;
+  if (r >= b) ++q;
+  return q;
 }
 
 // A position on the line, walked block by block over units and sequences.
@@ -161,16 +148,16 @@ struct Cursor {
   int s;            // sequence
   Seq q;
   int head, rg, blk;
-  long long unit_start;
-  __device__ __forceinline__ void begin(const Fp4AttnParams& p, int seq, long long pre,
-                                        long long pos) {
+  int unit_start;
+  // at position `pos` of the line, in sequence seq whose first unit starts at pre
+  __device__ __forceinline__ void begin(const Seq& sq, int seq, int pre, int pos) {
     s = seq;
-    q = load_seq<R>(p, s);
-    const long long o = pos - pre;
-    const long long u = o / q.nblk;
-    blk = (int)(o - u * q.nblk);
-    head = (int)(u / q.rgs);
-    rg = (int)(u - (long long)head * q.rgs);
+    q = sq;
+    const int o = pos - pre;
+    const int u = divide(o, q.nblk);
+    blk = o - u * q.nblk;
+    head = divide(u, q.rgs);
+    rg = u - head * q.rgs;
     unit_start = pos - blk;
   }
   // the next unit (only called while blocks of this line remain)
@@ -237,129 +224,203 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- the line of blocks, and this CTA's and its warps' stretches of it
-  long long total = 0;
-  for (int s0 = 0; s0 < p.num_seqs; s0 += W * 32) {
-    const int s = s0 + threadIdx.x;
-    long long part;
-    block_scan<W>(s < p.num_seqs ? seq_cost<R>(p, s) : 0, sh.scan, &part);
-    total += part;
-  }
-  // at least a block per warp: fewer CTAs take a short line
-  const long long per = max((total + gridDim.x - 1) / (long long)gridDim.x, (long long)W);
-  const long long cta0 = blockIdx.x * per, cta1 = min(total, cta0 + per);
-  if (cta0 >= total) return;
-  const int len = (int)(cta1 - cta0);
-  auto warp_start = [&](int w) { return cta0 + (long long)len * w / W; };
-  {
-    long long base = 0;
-    for (int s0 = 0; s0 < p.num_seqs && base < cta1; s0 += W * 32) {
-      const int s = s0 + threadIdx.x;
-      const long long c = s < p.num_seqs ? seq_cost<R>(p, s) : 0;
-      long long part;
-      const long long end = base + block_scan<W>(c, sh.scan, &part);
-      if (c > 0 && end > cta0 && end - c < cta1)
-        for (int w = 0; w < W; ++w) {
-          const long long at = warp_start(w);
-          if (at >= end - c && at < end) {
-            sh.start_seq[w] = s;
-            sh.start_pre[w] = end - c;
-          }
+  // ---- the line of blocks (under 2^31 of them, which the host checks): its
+  // length, this CTA's stretch of it and this warp's stretch of that, one step
+  // each.  Up to W * 32 sequences stay in shared memory between the steps (one
+  // barrier in all); more are gone over again in each.  Every warp searches
+  // the sums itself.
+  const bool resident = p.num_seqs <= W * 32;
+  int per = 0, cta0 = 0, cta1 = 0;
+  auto warp_start = [&](int w) { return cta0 + (int)((unsigned)(cta1 - cta0) * w / W); };
+  Cursor<R> cu{};  // the arithmetic's
+#pragma unroll 1
+  for (int step = 0; step < 3; ++step) {
+    int base = 0;
+#pragma unroll 1
+    for (int s0 = 0; s0 < p.num_seqs; s0 += W * 32) {
+      if (step == 0 || !resident) {
+        const int s = s0 + threadIdx.x;
+        const Seq sq = s < p.num_seqs ? load_seq<R>(p, s) : Seq{};
+        int sum = sq.nblk * sq.rgs * p.num_kv_heads;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += y;
         }
-      base += part;
+        if (s0 > 0 || step > 0) __syncthreads();  // the ones before have been searched
+        sh.seqs[threadIdx.x] = make_int4(sq.q0, sq.ql, sq.L, sum);
+        __syncthreads();
+      }
+      // lane w: the blocks up to the end of warp w's sequences
+      int upto = lane < W ? sh.seqs[lane * 32 + 31].w : 0;
+#pragma unroll
+      for (int o = 1; o < W; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      upto += base;
+      // the sequence (of those in shared memory) that holds position `at`;
+      // *pre: where it starts
+      auto find = [&](int at, int* pre) {
+        const int w = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
+        const int before = w == 0 ? base : __shfl_sync(0xffffffffu, upto, w - 1);
+        const int end = sh.seqs[w * 32 + lane].w + before;
+        const int i = __ffs(__ballot_sync(0xffffffffu, end > at)) - 1;
+        const int up = __shfl_sync(0xffffffffu, end, max(i - 1, 0));
+        *pre = i == 0 ? before : up;
+        return w * 32 + i;
+      };
+      const int end = __shfl_sync(0xffffffffu, upto, W - 1);
+      if (step == 1) {
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          int at = min((long long)(blockIdx.x + i) * per, (long long)INT32_MAX);
+          if (at < base || at >= end) continue;
+          int pre;
+          const int nblk = (sh.seqs[find(at, &pre)].z + kBlockSize - 1) / kBlockSize;
+          const int r = at - pre - divide(at - pre, nblk) * nblk;
+          if (nblk <= S::kWhole) at += 2 * r < nblk ? -r : nblk - r;
+          (i == 0 ? cta0 : cta1) = at;
+        }
+      }
+      if (step == 2) {
+        const int at = warp_start(warp);
+        if (at >= base && at < end) {
+          int pre;
+          const int i = find(at, &pre);
+          const int4 q = sh.seqs[i];
+          cu.begin(make_seq<R>(p, q.x, q.y, q.z), s0 + i, pre, at);
+        }
+      }
+      base = end;
     }
+    if (step == 0) {
+      // at least a block per warp: fewer CTAs take a short line
+      per = max(divide(base + (int)gridDim.x - 1, (int)gridDim.x), W);
+      if ((long long)blockIdx.x * per >= base) return;
+      cta0 = cta1 = base;
+    }
+    if (step == 1 && cta0 >= cta1) return;
   }
-  __syncthreads();
 
-  const long long pos0 = warp_start(warp), pos1 = warp_start(warp + 1);
+  const int pos0 = warp_start(warp), pos1 = warp_start(warp + 1);
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + S::ring_off) + warp * S::kRing;
   const uint32_t bars = (uint32_t)__cvta_generic_to_shared(&sh.bars[warp * S::kStages]);
   bool ok = true;
 
   if (pos1 > pos0) {
-    // ---- loads: a cursor of their own, kStages blocks ahead of the arithmetic
-    Cursor<R> ld;
-    ld.begin(p, sh.start_seq[warp], sh.start_pre[warp], pos0);
-    int left = (int)(pos1 - pos0);  // blocks not yet issued
-    int issued = 0;
-    int ids = 0, ids_at = -1;       // lane i: the id of block ids_at + i of the sequence
-    auto issue = [&]() {
-      if (ids_at < 0 || ld.blk >= ids_at + 32) {
-        ids_at = ld.blk;
-        const int b = min(ids_at + lane, ld.q.nblk - 1);
-        ids = p.block_tables[(int64_t)ld.s * p.max_blocks_per_seq + b];
-        ids = min(max(ids, 0), p.num_blocks - 1);  // never outside the pool
+    // ---- loads: in pairs of blocks of one unit (the last of an odd number
+    // alone), a ring ahead of the arithmetic and with a cursor of their own.
+    // Lane i holds the tiles of the i-th pair of a window of 32, and the block
+    // ids of the window after it, on their way from the block table.
+    Cursor<R> ld = cu;
+    int ahead = pos1 - pos0;            // blocks not yet in a window
+    int left = 0;                       // pairs of this window not yet issued
+    int at_lane = 0, put = 0;           // the next one, and its stage
+    int tile0 = 0, tile1 = 0;           // (second tile -1: none)
+    int next0 = 0, next1 = 0, next_head = 0, next_pairs = 0;
+    auto clamp_id = [&](int id) { return min(max(id, 0), p.num_blocks - 1); };  // never outside the pool
+    auto look_ahead = [&]() {
+      int n = 0, blk = -1, seq = 0;
+      bool both = false;
+      while (n < 32 && ahead > 0) {
+        const int here = min(ld.q.nblk - ld.blk, ahead);      // blocks of this unit
+        const int pairs = min((here + 1) / 2, 32 - n);
+        if (lane >= n && lane < n + pairs) {
+          blk = ld.blk + 2 * (lane - n);
+          both = 2 * (lane - n) + 1 < here;
+          seq = ld.s;
+          next_head = ld.head;
+        }
+        n += pairs;
+        const int took = min(2 * pairs, here);
+        ahead -= took;
+        ld.blk += took;
+        if (ld.blk == ld.q.nblk && ahead > 0) ld.next_unit(p);
       }
-      const int id = __shfl_sync(0xffffffffu, ids, ld.blk - ids_at);
-      if (lane == 0) {
-        const int st = issued % S::kStages;
-        mbar_expect_tx(bars + 8 * st, S::kTile);
-        bulk_load(ring + st * S::kTile,
-                  p.kv_cache + ((int64_t)id * p.num_kv_heads + ld.head) * S::kTile, S::kTile,
-                  bars + 8 * st);
-      }
-      ++issued;
-      --left;
-      if (++ld.blk == ld.q.nblk) {
-        const int was = ld.s;
-        if (left > 0) ld.next_unit(p);
-        if (ld.s != was || ids_at > 0) ids_at = -1;
-      }
+      next_pairs = n;
+      const int32_t* ids = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
+      next0 = blk >= 0 ? ids[blk] : 0;
+      next1 = both ? ids[blk + 1] : INT32_MIN;
     };
-    for (int i = 0; i < S::kStages && left > 0; ++i) issue();
+    auto issue = [&]() {  // the next pair, if there is one
+      if (left == 0) {
+        if (next_pairs == 0) return;
+        left = next_pairs;
+        at_lane = 0;
+        tile0 = clamp_id(next0) * p.num_kv_heads + next_head;
+        tile1 = next1 == INT32_MIN ? -1 : clamp_id(next1) * p.num_kv_heads + next_head;
+        look_ahead();
+      }
+      if (lane == at_lane) {
+        const uint32_t bar = bars + 8 * put, dst = ring + put * 2 * S::kTile;
+        mbar_expect_tx(bar, tile1 < 0 ? S::kTile : 2 * S::kTile);
+        bulk_load(dst, p.kv_cache + (int64_t)tile0 * S::kTile, S::kTile, bar);
+        if (tile1 >= 0)
+          bulk_load(dst + S::kTile, p.kv_cache + (int64_t)tile1 * S::kTile, S::kTile, bar);
+      }
+      ++at_lane;
+      --left;
+      put = put + 1 == S::kStages ? 0 : put + 1;
+    };
 
     // ---- the units of this stretch
-    Cursor<R> cu;
-    cu.begin(p, sh.start_seq[warp], sh.start_pre[warp], pos0);
-    long long pos = pos0;
-    int done = 0;
+    int pos = pos0;
+    int at = 0, phase = 0;  // stage of the next block, and its barrier's parity
+    bool first = true;
     while (pos < pos1 && ok) {
       const int blk0 = cu.blk;
-      const int nb = (int)min((long long)(cu.q.nblk - blk0), pos1 - pos);
+      const int nb = min(cu.q.nblk - blk0, pos1 - pos);
       const int nrows = min(R, cu.q.ql * p.group - cu.rg * R);
       // -- the query rows (the B operand): row g (+8), this lane's chunk of dims
+      constexpr int kVecs = S::kChunkK * (int)sizeof(T) / 16;
+      uint4 raw[NT][kVecs];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int row = n * 8 + g;
+        const int rr = cu.rg * R + row, j = divide(rr, p.group);
+        const T* src = (const T*)p.q +
+                       ((int64_t)(cu.q.q0 + j) * p.num_q_heads + cu.head * p.group +
+                        (rr - j * p.group)) * D +
+                       t * S::kChunkK;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+          raw[n][i] = row < nrows ? ((const uint4*)src)[i] : make_uint4(0, 0, 0, 0);
+      }
+      if (first) {  // the first tiles' loads leave while the query's are under way
+        look_ahead();
+        for (int i = 0; i < S::kStages; ++i) issue();
+        first = false;
+      }
       uint32_t qf[QP][NT][K][2];
       float sl2[NT][2];  // log2(e) scale of the scores of rows 2t, 2t+1 (+8)
       int lim[NT][2];    // their last visible key
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int row = n * 8 + g;
-        const int rr = cu.rg * R + row;
         float x[S::kChunkK];
-        if (row < nrows) {
-          const int j = rr / p.group;
-          const T* src = (const T*)p.q +
-                         ((int64_t)(cu.q.q0 + j) * p.num_q_heads + cu.head * p.group +
-                          (rr - j * p.group)) * D +
-                         t * S::kChunkK;
 #pragma unroll
-          for (int i = 0; i < S::kChunkK; i += 16 / (int)sizeof(T)) {
-            const uint4 w = *(const uint4*)(src + i);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int i = 0; i < kVecs; ++i) {
+          const uint32_t u[4] = {raw[n][i].x, raw[n][i].y, raw[n][i].z, raw[n][i].w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if constexpr (sizeof(T) == 2) {
-                x[i + 2 * k] = __uint_as_float(u[k] << 16);
-                x[i + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-              } else {
-                x[i + k] = __uint_as_float(u[k]);
-              }
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (sizeof(T) == 2) {
+              x[8 * i + 2 * k] = __uint_as_float(u[k] << 16);
+              x[8 * i + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+            } else {
+              x[4 * i + k] = __uint_as_float(u[k]);
             }
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < S::kChunkK; ++i) x[i] = 0.f;
         }
         float mx = 0.f;
 #pragma unroll
         for (int i = 0; i < S::kChunkK; ++i) mx = fmaxf(mx, fabsf(x[i]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // the exponent of the row's largest value; 0 for a row of zeros and
-        // (as they are) for infinities.  Two factors: 2^-e alone may overflow
-        const int e = mx > 0.f && mx < INFINITY ? ilogbf(mx) : 0;
-        const int e1 = -e / 2;
-        const float f1 = __int_as_float((127 + e1) << 23), f2 = __int_as_float((127 - e - e1) << 23);
+        // the exponent of the row's largest value (-127 for subnormals and
+        // zeros; infinities and NaN stay what they are).  Two factors: 2^127
+        // and 2^-128 alone are no normal fp32 numbers
+        const int e = (__float_as_int(mx) >> 23) - 127, e1 = e / 2;
+        const float f1 = exp2i(-e1), f2 = exp2i(e1 - e);
 #pragma unroll
         for (int i = 0; i < S::kChunkK; ++i) x[i] = x[i] * f1 * f2;
 #pragma unroll
@@ -377,9 +438,9 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int er = __shfl_sync(0xffffffffu, e, (2 * t + c) * 4);
-          sl2[n][c] = ldexpf(p.scale_log2, er);
+          sl2[n][c] = p.scale_log2 * exp2i(er / 2) * exp2i(er - er / 2);
           const int r2 = cu.rg * R + n * 8 + 2 * t + c;
-          lim[n][c] = n * 8 + 2 * t + c < nrows ? cu.q.L - cu.q.ql + r2 / p.group : cu.q.L - 1;
+          lim[n][c] = n * 8 + 2 * t + c < nrows ? cu.q.L - cu.q.ql + divide(r2, p.group) : cu.q.L - 1;
         }
       }
 
@@ -395,103 +456,124 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
         l[n][0] = l[n][1] = 0.f;
       }
 
-      for (int b = 0; b < nb; ++b, ++done) {
-        const int st = done % S::kStages;
-        ok = wait_bar(bars + 8 * st, (done / S::kStages) & 1, abort_flag, p.ws_status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const unsigned char* tile = smem + S::ring_off + warp * S::kRing + st * S::kTile;
-        // -- this lane's codes and scales: K of tokens ta and ta + 2, V of
-        // tokens 4t .. 4t + 3
-        const int ta = 4 * (g >> 1) + (g & 1);
-        uint32_t kw[2][K / 2], vw[2][K / 2];
-        uint32_t ks[2], vs;
-        if constexpr (D == 128) {
+      // -- two blocks at a time (the second of the last pair may be none: its
+      // scores are all masked, and its V counts as 0)
+      const int ta = 4 * (g >> 1) + (g & 1);  // K rows: tokens ta, ta + 2; V: 4t .. 4t + 3
+      for (int b = 0; b < nb; b += 2) {
+        const int two = nb - b == 1 ? 1 : 2;
+        uint32_t kw[2][2][K / 2], vw[2][2][K / 2], ks[2][2], vs[2];
+        if (!__all_sync(0xffffffffu, mbar_try_wait(bars + 8 * at, phase))) {
+          ok = wait_bar(bars + 8 * at, phase, abort_flag, p.ws_status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        const unsigned char* stage = smem + S::ring_off + warp * S::kRing + at * 2 * S::kTile;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 a = *(const uint4*)(tile + (ta + 2 * h) * 64 + t * 16);
-            kw[h][0] = a.x; kw[h][1] = a.y; kw[h][2] = a.z; kw[h][3] = a.w;
-            const uint4 v = *(const uint4*)(tile + Tile::v_off + h * 512 + lane * 16);
-            vw[h][0] = v.x; vw[h][1] = v.y; vw[h][2] = v.z; vw[h][3] = v.w;
-            ks[h] = *(const uint16_t*)(tile + Tile::ks_off + (ta + 2 * h) * 8 + 2 * t);
-          }
-          vs = *(const uint32_t*)(tile + Tile::vs_off + g * 16 + 4 * t);
-        } else {
+        for (int i = 0; i < 2; ++i) {
+          const unsigned char* tile = stage + i * S::kTile;
+          if constexpr (D == 128) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint2 a = *(const uint2*)(tile + (ta + 2 * h) * 32 + t * 8);
-            kw[h][0] = a.x; kw[h][1] = a.y;
-            const uint2 v = *(const uint2*)(tile + Tile::v_off + h * 256 + lane * 8);
-            vw[h][0] = v.x; vw[h][1] = v.y;
-            ks[h] = *(tile + Tile::ks_off + (ta + 2 * h) * 4 + t);
+            for (int h = 0; h < 2; ++h) {
+              const uint4 a = *(const uint4*)(tile + (ta + 2 * h) * 64 + t * 16);
+              kw[i][h][0] = a.x; kw[i][h][1] = a.y; kw[i][h][2] = a.z; kw[i][h][3] = a.w;
+              const uint4 v = *(const uint4*)(tile + Tile::v_off + h * 512 + lane * 16);
+              vw[i][h][0] = v.x; vw[i][h][1] = v.y; vw[i][h][2] = v.z; vw[i][h][3] = v.w;
+              ks[i][h] = *(const uint16_t*)(tile + Tile::ks_off + (ta + 2 * h) * 8 + 2 * t);
+            }
+            vs[i] = *(const uint32_t*)(tile + Tile::vs_off + g * 16 + 4 * t);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint2 a = *(const uint2*)(tile + (ta + 2 * h) * 32 + t * 8);
+              kw[i][h][0] = a.x; kw[i][h][1] = a.y;
+              const uint2 v = *(const uint2*)(tile + Tile::v_off + h * 256 + lane * 8);
+              vw[i][h][0] = v.x; vw[i][h][1] = v.y;
+              ks[i][h] = *(tile + Tile::ks_off + (ta + 2 * h) * 4 + t);
+            }
+            vs[i] = *(const uint32_t*)(tile + Tile::vs_off + (g >> 1) * 16 + 4 * t);
           }
-          vs = *(const uint32_t*)(tile + Tile::vs_off + (g >> 1) * 16 + 4 * t);
+        }
+        if (++at == S::kStages) {
+          at = 0;
+          phase ^= 1;
         }
         __syncwarp();  // the stage is free once every lane holds its part of it
-        if (left > 0) issue();
+        issue();
 
-        // -- S^T = K Q^T in two chains of MMAs
-        float sc[NT][2][4];
+        // -- S^T = K Q^T: scores in log2 units
+        float x[2][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sc[n][0][c] = sc[n][1][c] = 0.f;
-        __half2 k2[2][2];  // [token][group of the chunk]
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const __half2 two = e4m3x2_to_half2(ks[h]);
-          k2[h][0] = __low2half2(two);
-          k2[h][1] = __high2half2(two);
-        }
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          const int grp = D == 128 ? k / 4 : 0;
-          const uint32_t w0 = kw[0][k / 2] >> (16 * (k & 1)), w1 = kw[1][k / 2] >> (16 * (k & 1));
-          const uint32_t a0 = deq<0>(w0, k2[0][grp]), a1 = deq<0>(w1, k2[1][grp]);
-          const uint32_t a2 = deq<1>(w0, k2[0][grp]), a3 = deq<1>(w1, k2[1][grp]);
+        for (int i = 0; i < 2; ++i) {
+          float sc[NT][2][4];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int qp = 0; qp < QP; ++qp)
-              mma_f16(sc[n][k & 1], a0, a1, a2, a3, qf[qp][n][k][0], qf[qp][n][k][1]);
+            for (int c = 0; c < 4; ++c) sc[n][0][c] = sc[n][1][c] = 0.f;
+          __half2 k2[2][2];  // [token][group of the chunk]
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const __half2 pair = e4m3x2_to_half2(ks[i][h]);
+            k2[h][0] = __low2half2(pair);
+            k2[h][1] = __high2half2(pair);
+          }
+#pragma unroll
+          for (int w = 0; w < K / 2; ++w) {
+            const int grp = D == 128 ? w / 2 : 0;
+            uint32_t a[2][4];
+            deq8(kw[i][0][w], k2[0][grp], a[0]);
+            deq8(kw[i][1][w], k2[1][grp], a[1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int qp = 0; qp < QP; ++qp)
+                  mma_f16(sc[n][j], a[0][2 * j], a[1][2 * j], a[0][2 * j + 1], a[1][2 * j + 1],
+                          qf[qp][n][2 * w + j][0], qf[qp][n][2 * w + j][1]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[i][n][c] = (sc[n][0][c] + sc[n][1][c]) * sl2[n][c & 1];
         }
-        // -- scores in log2 units; keys past a row's last visible one are out
-        float x[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[n][c] = (sc[n][0][c] + sc[n][1][c]) * sl2[n][c & 1];
+        // -- keys past a row's last visible one are out
         const int key0 = (blk0 + b) * kBlockSize;
-        if (key0 + kBlockSize > cu.q.L - cu.q.ql + 1) {
+        if (key0 + 2 * kBlockSize > cu.q.L - cu.q.ql + 1 || two == 1) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int i = 0; i < 2; ++i) {
+            const int key = i < two ? key0 + i * kBlockSize : INT32_MAX - 64;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (key0 + ta + (c & 2) > lim[n][c & 1]) x[n][c] = -INFINITY;
-          // V of slots that hold no token yet: whatever they hold counts as 0
-          const int held = cu.q.L - key0 - 4 * t;
-          if (held < 4) vs = held <= 0 ? 0u : vs & (0xffffffffu >> (32 - 8 * held));
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (key + ta + (c & 2) > lim[n][c & 1]) x[i][n][c] = -INFINITY;
+            // V of slots that hold no token: whatever they hold counts as 0
+            const int held = cu.q.L - key - 4 * t;
+            if (held < 4) vs[i] = held <= 0 ? 0u : vs[i] & (0xffffffffu >> (32 - 8 * held));
+          }
         }
         // -- the running max moves when a score passes it by 2^8
+        float mx[NT][2];
         bool over = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            over |= fmaxf(x[n][c], x[n][c + 2]) > m[n][c] + kRescale ||
-                    (m[n][c] == -INFINITY && fmaxf(x[n][c], x[n][c + 2]) > -INFINITY);
+          for (int c = 0; c < 2; ++c) {
+            mx[n][c] = fmaxf(fmaxf(x[0][n][c], x[0][n][c + 2]), fmaxf(x[1][n][c], x[1][n][c + 2]));
+            // (a max of -inf is passed by every score but -inf)
+            over |= mx[n][c] > m[n][c] + kRescale;
+          }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float mx = fmaxf(x[n][c], x[n][c + 2]);
+              float v = mx[n][c];
 #pragma unroll
-              for (int s = 4; s < 32; s <<= 1)
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-              if (mx > m[n][c] + kRescale || (m[n][c] == -INFINITY && mx > -INFINITY)) {
-                const float f = ex2(m[n][c] - mx);
-                m[n][c] = mx;
+              for (int s = 4; s < 32; s <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
+              if (v > m[n][c] + kRescale) {
+                const float f = ex2(m[n][c] - v);
+                m[n][c] = v;
                 l[n][c] *= f;
 #pragma unroll
                 for (int i = 0; i < K; ++i) {
@@ -502,53 +584,53 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
             }
         }
         // -- P^T in f16
-        uint32_t pf[QP][NT][2];
+        uint32_t pf[2][QP][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float e[4];
+          float base[2];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float base = m[n][c & 1] == -INFINITY ? 0.f : m[n][c & 1] - kPShift;
-            e[c] = ex2(x[n][c] - base);
-          }
-          l[n][0] += e[0] + e[2];
-          l[n][1] += e[1] + e[3];
+          for (int c = 0; c < 2; ++c) base[c] = m[n][c] == -INFINITY ? 0.f : m[n][c] - kPShift;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const __half2 hi = __floats2half2_rn(e[2 * h], e[2 * h + 1]);
-            pf[0][n][h] = transpose8(bits(hi));
-            if constexpr (QP == 2)
-              pf[QP - 1][n][h] = transpose8(bits(__floats2half2_rn(
-                  e[2 * h] - __low2float(hi), e[2 * h + 1] - __high2float(hi))));
+          for (int i = 0; i < 2; ++i) {
+            float e[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) e[c] = ex2(x[i][n][c] - base[c & 1]);
+            l[n][0] += e[0] + e[2];
+            l[n][1] += e[1] + e[3];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const __half2 hi = __floats2half2_rn(e[2 * h], e[2 * h + 1]);
+              pf[i][0][n][h] = transpose8(bits(hi));
+              if constexpr (QP == 2)
+                pf[i][QP - 1][n][h] = transpose8(bits(__floats2half2_rn(
+                    e[2 * h] - __low2float(hi), e[2 * h + 1] - __high2float(hi))));
+            }
           }
         }
         // -- O^T += V^T P^T: the codes of a pair of tokens side by side in a
         // byte (even dims, odd dims), converted and scaled
-        const __half2 v2[2] = {e4m3x2_to_half2(vs & 0xffffu), e4m3x2_to_half2(vs >> 16)};
         constexpr uint32_t kLow = 0x0f0f0f0fu;
 #pragma unroll
-        for (int w = 0; w < K / 4; ++w) {
-          uint32_t ev[2], od[2];
+        for (int i = 0; i < 2; ++i) {
+          const __half2 v2[2] = {e4m3x2_to_half2(vs[i] & 0xffffu), e4m3x2_to_half2(vs[i] >> 16)};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a = vw[h][w], c = vw[h][K / 4 + w];
-            ev[h] = (a & kLow) | ((c << 4) & ~kLow);
-            od[h] = ((a >> 4) & kLow) | (c & ~kLow);
+          for (int w = 0; w < K / 4; ++w) {
+            uint32_t ev[2][4], od[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a = vw[i][h][w], c = vw[i][h][K / 4 + w];
+              deq8((a & kLow) | ((c << 4) & ~kLow), v2[h], ev[h]);
+              deq8(((a >> 4) & kLow) | (c & ~kLow), v2[h], od[h]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int qp = 0; qp < QP; ++qp)
+                  mma_f16(o[n][4 * w + k], ev[0][k], od[0][k], ev[1][k], od[1][k],
+                          pf[i][qp][n][0], pf[i][qp][n][1]);
           }
-          auto step = [&](auto ic) {
-            constexpr int i = decltype(ic)::value;
-            const uint32_t a0 = deq<i>(ev[0], v2[0]), a1 = deq<i>(od[0], v2[0]);
-            const uint32_t a2 = deq<i>(ev[1], v2[1]), a3 = deq<i>(od[1], v2[1]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int qp = 0; qp < QP; ++qp)
-                mma_f16(o[n][4 * w + i], a0, a1, a2, a3, pf[qp][n][0], pf[qp][n][1]);
-          };
-          step(std::integral_constant<int, 0>{});
-          step(std::integral_constant<int, 1>{});
-          step(std::integral_constant<int, 2>{});
-          step(std::integral_constant<int, 3>{});
         }
       }
       if (!ok) break;
@@ -574,7 +656,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
             y[2 * i + 1] = o[n][i][c + 2] * f;
           }
           if (whole) {
-            const int rr = cu.rg * R + row, j = rr / p.group;
+            const int rr = cu.rg * R + row, j = divide(rr, p.group);
             store_row((T*)p.out +
                           ((int64_t)(cu.q.q0 + j) * p.num_q_heads + cu.head * p.group +
                            (rr - j * p.group)) * D +
@@ -595,9 +677,10 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
         PartMeta& pm = sh.meta[warp][slot];
         pm.unit_start = cu.unit_start;
         pm.nblk = cu.q.nblk;
-        pm.seq = cu.s;
+        pm.q0 = cu.q.q0;
         pm.head = cu.head;
-        pm.rg = cu.rg;
+        pm.row0 = cu.rg * R;
+        pm.nrows = nrows;
         pm.ended = blk0 + nb == cu.q.nblk;
         pm.valid = 1;
       }
@@ -641,15 +724,15 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
     const bool ended = end != 0;
     if (ended) mine &= (end & -end) | ((end & -end) - 1);
     const PartMeta& pm = sh.meta[w0][from_before ? 0 : 1];
-    const Seq q = load_seq<R>(p, pm.seq);
-    const int nrows = min(R, q.ql * p.group - pm.rg * R);
+    const int nrows = pm.nrows;
     const bool complete = ended && !from_before;
     const int side = from_before ? 0 : 1;
     if (!complete) {
       pending[side] = true;
       far[side] = pm;
     }
-    for (int row = warp; row < nrows; row += W) {
+    // the rows of all runs go round the warps
+    for (int row = (warp + W * R - r * R) % W; row < nrows; row += W) {
       // weights of the parts: lane w that of warp w's first part, lane 31 that
       // of the part the unit starts with
       float mi = -INFINITY, li = 0.f;
@@ -670,19 +753,25 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
       float y[D / 32];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) y[i] = 0.f;
-      auto add = [&](const float* part, float f) {
+      const int off = row * D + lane * (D / 32);
+      float v[W + 1][D / 32];  // the parts, all their loads before any sum
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) y[i] = fmaf(f, part[row * D + lane * (D / 32) + i], y[i]);
-      };
-      if (!from_before)
-        add((const float*)(smem + S::ring_off + w0 * S::kRing), __shfl_sync(0xffffffffu, wt, 31));
-      for (unsigned left = mine; left; left &= left - 1) {
-        const int w = __ffs(left) - 1;
-        add((const float*)(smem + S::part_off + w * S::kPart), __shfl_sync(0xffffffffu, wt, w));
+      for (int w = 0; w <= W; ++w) {
+        const float* part = (const float*)(w < W ? smem + S::part_off + w * S::kPart
+                                                 : smem + S::ring_off + w0 * S::kRing) + off;
+        const bool in = w < W ? mine >> w & 1 : !from_before;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) v[w][i] = in ? part[i] : 0.f;
+      }
+#pragma unroll
+      for (int w = W; w >= 0; --w) {
+        const float f = __shfl_sync(0xffffffffu, wt, w < W ? w : 31);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) y[i] = fmaf(f, v[w][i], y[i]);
       }
       if (complete) {
-        const int rr = pm.rg * R + row, j = rr / p.group;
-        T* dst = (T*)p.out + ((int64_t)(q.q0 + j) * p.num_q_heads + pm.head * p.group +
+        const int rr = pm.row0 + row, j = divide(rr, p.group);
+        T* dst = (T*)p.out + ((int64_t)(pm.q0 + j) * p.num_q_heads + pm.head * p.group +
                               (rr - j * p.group)) * D + lane * (D / 32);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) dst[i] = (T)(y[i] * (p.v_scale / sum));
@@ -707,7 +796,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
     int mine = 0;
     if (pending[threadIdx.x]) {
       const PartMeta& f = far[threadIdx.x];
-      const int c0 = (int)(f.unit_start / per), c1 = (int)((f.unit_start + f.nblk - 1) / per);
+      const int c0 = divide(f.unit_start, per), c1 = divide(f.unit_start + f.nblk - 1, per);
       mine = atomicAdd(p.ws_counters + c0, 1) == c1 - c0;
       if (mine) p.ws_counters[c0] = 0;  // every part has arrived: zero for the next call
     }
@@ -719,29 +808,36 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
     if (!sh.last[side]) continue;
     __threadfence();
     const PartMeta f = far[side];
-    const Seq q = load_seq<R>(p, f.seq);
-    const int nrows = min(R, q.ql * p.group - f.rg * R);
-    const int c0 = (int)(f.unit_start / per), c1 = (int)((f.unit_start + f.nblk - 1) / per);
-    for (int row = warp; row < nrows; row += W) {
-      auto at = [&](int c) { return (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * 16 + row; };
+    const int c0 = divide(f.unit_start, per), c1 = divide(f.unit_start + f.nblk - 1, per);
+    for (int row = warp; row < f.nrows; row += W) {
+      auto slot = [&](int c) { return (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * 16 + row; };
       float mx = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, __ldcg(p.ws_ml + at(c) * 2));
+      for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, __ldcg(p.ws_ml + slot(c) * 2));
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
       float y[D / 32], sum = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) y[i] = 0.f;
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const float mi = __ldcg(p.ws_ml + at(c) * 2);
-        const float wt = mi == -INFINITY ? 0.f : ex2(mi - mx);
-        sum = fmaf(wt, __ldcg(p.ws_ml + at(c) * 2 + 1), sum);
+      for (int cc = c0; cc <= c1; cc += 32) {  // a lane's weight each, then the parts
+        const int c = cc + lane;
+        float wt = 0.f;
+        if (c <= c1) {
+          const float2 ml = __ldcg((const float2*)(p.ws_ml + slot(c) * 2));
+          wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
+          sum = fmaf(wt, ml.y, sum);
+        }
+#pragma unroll 8
+        for (int i = cc; i <= min(c1, cc + 31); ++i) {
+          const float f1 = __shfl_sync(0xffffffffu, wt, i - cc);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          y[i] = fmaf(wt, __ldcg(p.ws_o + at(c) * D + lane * (D / 32) + i), y[i]);
+          for (int k = 0; k < D / 32; ++k)
+            y[k] = fmaf(f1, __ldcg(p.ws_o + slot(i) * D + lane * (D / 32) + k), y[k]);
+        }
       }
-      const int rr = f.rg * R + row, j = rr / p.group;
-      T* dst = (T*)p.out + ((int64_t)(q.q0 + j) * p.num_q_heads + f.head * p.group +
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+      const int rr = f.row0 + row, j = divide(rr, p.group);
+      T* dst = (T*)p.out + ((int64_t)(f.q0 + j) * p.num_q_heads + f.head * p.group +
                             (rr - j * p.group)) * D + lane * (D / 32);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) dst[i] = (T)(y[i] * (p.v_scale / sum));

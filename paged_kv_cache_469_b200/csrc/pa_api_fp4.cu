@@ -202,6 +202,10 @@ extern "C" int pa_attention_varlen_fp4(
     }
     rows = longest * group;
   }
+  // the decode kernel's line of blocks is counted in 32 bits
+  const double groups = num_seqs + (double)num_tokens * group / (rows > 8 ? 16 : 8);
+  if (groups * num_kv_heads * ((max_seq_len + kBlockSize - 1) / kBlockSize) >= 2147483648.0)
+    return PA_ERR_UNSUPPORTED;
   const Fp4Workspace w = fp4_workspace(head_dim);
   if (!workspace || workspace_bytes < w.total || !aligned_to(workspace, 16)) return PA_ERR_INVALID;
   char* ws = (char*)workspace;
@@ -222,7 +226,7 @@ extern "C" int pa_attention_varlen_fp4(
   p.num_blocks = num_blocks;
   p.scale_log2 = scale * k_scale * 1.4426950408889634f;
   p.v_scale = v_scale;
-  p.max_rows = INT32_MAX;
+  p.max_q = INT32_MAX;
   p.ws_status = (int*)ws;
   p.ws_counters = (int*)(ws + w.counters_off);
   p.ws_ml = (float*)(ws + w.ml_off);

@@ -199,7 +199,7 @@ struct Fp4AttnParams {
   int num_blocks;
   float scale_log2;  // scale * k_scale * log2(e)
   float v_scale;
-  int max_rows;      // decode kernel: sequences with more query rows per kv-head are not its own
+  int max_q;         // decode kernel: sequences with more query tokens are not its own
   int* ws_status;    // the workspace header
   int* ws_counters;  // [kFp4MaxCtas]: arrivals at a unit that starts in that CTA, zero between calls
   float* ws_ml;      // [kFp4MaxCtas][2][16][2] running max (log2 units) and sum

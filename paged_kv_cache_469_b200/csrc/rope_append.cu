@@ -277,9 +277,11 @@ gather_fp4_kernel(const GatherFp4Params p, int64_t threads) {
   for (int j = 0; j < 4; ++j) {
     const float sc = s[j / 2], own = j < 2 ? p.k_scale : p.v_scale;
     float x[8];
+    __half2 two[4];
+    e2m1x8_to_half2(w[j], two);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 f = __half22float2(e2m1x2_to_half2(w[j] >> (8 * e) & 255u));
+      const float2 f = __half22float2(two[e]);
       x[2 * e] = __fmul_rn(f.x * sc, own);  // code * scale is exact
       x[2 * e + 1] = __fmul_rn(f.y * sc, own);
     }
