@@ -90,16 +90,22 @@ int rope_append_impl(void* q_out, const void* q, int64_t q_stride, const void* k
 }
 
 // Workspace of attention over a 4-bit cache: the 256-byte header, the arrival
-// counters, and two partial results per CTA.
+// counters, two partial results per CTA, and the prefill work list.
 struct Fp4Workspace {
-  size_t counters_off, ml_off, o_off, total;
+  int max_items;
+  size_t counters_off, ml_off, o_off, items_off, total;
 };
-Fp4Workspace fp4_workspace(int head_dim) {
+Fp4Workspace fp4_workspace(int num_seqs, int num_tokens, int num_q_heads, int head_dim) {
   Fp4Workspace w{};
   w.counters_off = 256;
   w.ml_off = w.counters_off + kFp4MaxCtas * sizeof(int);
   w.o_off = w.ml_off + (size_t)kFp4MaxCtas * 2 * 16 * 2 * sizeof(float);
-  w.total = w.o_off + (size_t)kFp4MaxCtas * 2 * 16 * head_dim * sizeof(float);
+  w.items_off = w.o_off + (size_t)kFp4MaxCtas * 2 * 16 * head_dim * sizeof(float);
+  // a sequence's query tiles times the heads at most, one item each
+  const int64_t items =
+      ((int64_t)num_tokens / kPrefillQTile + min(num_seqs, num_tokens)) * num_q_heads;
+  w.max_items = (int)min(items, (int64_t)1 << 30);
+  w.total = w.items_off + ((size_t)w.max_items + 1) * sizeof(int4);
   return w;
 }
 
@@ -159,7 +165,7 @@ extern "C" size_t pa_attention_fp4_workspace_size(int num_seqs, int num_tokens, 
                                                   int num_kv_heads, int head_dim) {
   if (num_seqs < 0 || num_tokens < 0 || num_kv_heads <= 0 || num_q_heads <= 0) return 0;
   if (num_q_heads % num_kv_heads != 0 || !supported_dim(head_dim)) return 0;
-  return fp4_workspace(head_dim).total;
+  return fp4_workspace(num_seqs, num_tokens, num_q_heads, head_dim).total;
 }
 
 extern "C" int pa_attention_varlen_fp4(
@@ -189,24 +195,38 @@ extern "C" int pa_attention_varlen_fp4(
   if (!aligned_to(out, 16) || !aligned_to(q, 16) || !aligned_to(kv_cache, 16) ||
       !aligned_to(block_tables, 4) || !aligned_to(seq_lens, 4) || !aligned_to(query_start_loc, 4))
     return PA_ERR_INVALID;
-  int rows = (int)min((long)max_query_len * group, (long)INT32_MAX);
+  // ---- which kernels the step needs.  bf16 sequences of more than
+  // kDecodeMaxRows query rows per kv-head are the prefill kernel's
+  const bool f32 = dtype == PA_DTYPE_F32;
+  const int decode_q = f32 ? INT32_MAX : kDecodeMaxRows / group;  // most query tokens of the others
+  int longest = min(max_query_len, decode_q);                     // of the decode kernel's
+  bool any_decode = true, any_prefill = max_query_len > decode_q;
   if (seq_lens_host && query_start_loc_host) {
     if (query_start_loc_host[0] != 0 || query_start_loc_host[num_seqs] != num_tokens)
       return PA_ERR_INVALID;
-    int longest = 0;
+    longest = 0;
+    any_prefill = false;
     for (int s = 0; s < num_seqs; ++s) {
       const int ql = query_start_loc_host[s + 1] - query_start_loc_host[s];
       const int L = seq_lens_host[s];
       if (ql < 0 || ql > L || L > max_seq_len || ql > max_query_len) return PA_ERR_INVALID;
-      longest = max(longest, ql);
+      if (ql > decode_q)
+        any_prefill = true;
+      else
+        longest = max(longest, ql);
     }
-    rows = longest * group;
+    any_decode = longest > 0;
   }
-  // the decode kernel's line of blocks is counted in 32 bits
-  const double groups = num_seqs + (double)num_tokens * group / (rows > 8 ? 16 : 8);
-  if (groups * num_kv_heads * ((max_seq_len + kBlockSize - 1) / kBlockSize) >= 2147483648.0)
+  const int64_t rows = (int64_t)longest * group;
+  // the prefill plan keeps a counter per 128-key tile in shared memory
+  if (any_prefill && max_blocks_per_seq / (kPrefillKvTile / kBlockSize) > 50000)
     return PA_ERR_UNSUPPORTED;
-  const Fp4Workspace w = fp4_workspace(head_dim);
+  // the decode kernel's line of blocks is counted in 32 bits
+  const double groups =
+      num_seqs + min((double)num_tokens, (double)num_seqs * longest) * group / (rows > 8 ? 16 : 8);
+  if (any_decode && groups * num_kv_heads * ((max_seq_len + kBlockSize - 1) / kBlockSize) >= 2147483648.0)
+    return PA_ERR_UNSUPPORTED;
+  const Fp4Workspace w = fp4_workspace(num_seqs, num_tokens, num_q_heads, head_dim);
   if (!workspace || workspace_bytes < w.total || !aligned_to(workspace, 16)) return PA_ERR_INVALID;
   char* ws = (char*)workspace;
   Fp4AttnParams p{};
@@ -226,13 +246,36 @@ extern "C" int pa_attention_varlen_fp4(
   p.num_blocks = num_blocks;
   p.scale_log2 = scale * k_scale * 1.4426950408889634f;
   p.v_scale = v_scale;
-  p.max_q = INT32_MAX;
+  p.max_q = decode_q;
   p.ws_status = (int*)ws;
   p.ws_counters = (int*)(ws + w.counters_off);
   p.ws_ml = (float*)(ws + w.ml_off);
   p.ws_o = (float*)(ws + w.o_off);
-  return launch_decode_fp4(p, head_dim, dtype == PA_DTYPE_F32, rows, (cudaStream_t)stream) ==
-                 cudaSuccess
+  if (any_decode && launch_decode_fp4(p, head_dim, f32, (int)min(rows, (int64_t)INT32_MAX),
+                                      (cudaStream_t)stream) != cudaSuccess)
+    return PA_ERR_CUDA;
+  if (!any_prefill) return PA_OK;
+  AttnParams a{};
+  a.out = out;
+  a.q = q;
+  a.k_cache = kv_cache;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.query_start_loc = query_start_loc;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.max_seq_len = max_seq_len;
+  a.num_seqs = num_seqs;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = group;
+  a.num_blocks = num_blocks;
+  a.scale_log2 = p.scale_log2;
+  a.ws_status = p.ws_status;
+  a.ws_items = (int4*)(ws + w.items_off);
+  a.max_items = w.max_items;
+  return launch_prefill_fp4(a, v_scale, head_dim, max_query_len, seq_lens_host,
+                            query_start_loc_host, (cudaStream_t)stream) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }

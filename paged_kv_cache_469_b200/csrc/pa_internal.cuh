@@ -247,6 +247,11 @@ cudaError_t launch_prefill_tcgen05(const AttnParams& p, int head_dim, int max_qu
                                    const int32_t* query_start_loc_host, cudaStream_t stream,
                                    int max_ctas);
 
+// The same over a 4-bit cache (p.k_cache): p.scale_log2 holds its k_scale.
+cudaError_t launch_prefill_fp4(const AttnParams& p, float v_scale, int head_dim,
+                               int max_query_len, const int32_t* seq_lens_host,
+                               const int32_t* query_start_loc_host, cudaStream_t stream);
+
 // pa_attention_varlen without the side stream of a mixed step (the two
 // classes run one after the other): for the caller that must not create any
 // CUDA object (the static-scratch entry point).

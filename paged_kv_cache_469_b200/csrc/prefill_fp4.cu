@@ -1,0 +1,702 @@
+// prefill_fp4.cu -- tensor-core paged attention of prefill chunks over the 4-bit
+// cache.
+//
+// Page "LLM推論エンジンvLLMの内部構造を徹底解説": section "エンジンの中核" -- a
+// prefill is compute-bound; section "高度な機能群" -- a chunk attends to the
+// context cached before it as well as to itself; section "PagedAttentionの仕組み"
+// -- keys are read through the sequence's block table.
+//
+// Work items, tiles and the softmax are those of the bf16 prefill kernel: two
+// 128-row Q tiles that read the same keys, 128 keys at a time, S and O in tensor
+// memory, P written back over S.  What differs is how the operands arrive:
+//
+//   warps 8, 10, 11  read the codes and scales of the tile's eight blocks one
+//               phase ahead into registers (4.5 bits a value: 18 KB a tile),
+//               convert them to f16 -- code * scale is exact there -- and store
+//               them as the 128-byte swizzled K and V tiles that tcgen05.mma
+//               reads; slots past the sequence are stored as zeros.  About 115
+//               instructions a lane and block, a third of a tile's MMA time,
+//               on issue slots that the softmax leaves free.
+//   warp 8      also loads the bf16 Q tiles by TMA
+//   warps 0..7  turn their query rows to f16 in place, each row times a power of
+//               two that brings its largest value into [1, 2) (bf16's bits fit),
+//               then run the softmax; P is f16, 2^7 times itself (at most 2^15),
+//               so that its small values keep their bits
+//   warp 9      MMA issuer
+//
+// Every mbarrier wait is bounded by a time limit; a wait that runs out sets a
+// status bit in the workspace and the CTA winds down instead of hanging.
+#include <cuda.h>
+#include <math.h>
+
+#include "pa_fastmath.cuh"
+#include "pa_fp4.cuh"
+#include "pa_internal.cuh"
+#include "pa_prefill_plan.cuh"
+#include "pa_tcgen05.cuh"
+#include "pa_tma.cuh"
+#include "pa_wait.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kTileBlocks = KT / kBlockSize;    // 8 cache blocks per tile
+constexpr int kStages = 2;                      // K tiles, and V tiles
+constexpr int kThreads = 384;                   // 12 warps = 3 warpgroups
+constexpr int kWarpQ = 8, kWarpMma = 9;
+constexpr int kProducers = 3;                   // warps 8, 10, 11
+// Registers: 2 x 128 x 208 + 128 x 88 = 384 x 168
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch,
+              "register split exceeds the launch allocation");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 0, kTmemS = 256;    // + 128 * half
+constexpr float kRescaleThreshold = 8.0f;       // log2 units: move the max only past 2^8
+constexpr float kPShift = 7.0f;                 // P is held times 2^7
+constexpr int kMaxChains = 8;                   // independent max chains over a row of scores
+
+template <int D>
+struct Layout {
+  static constexpr int kPanels = D / 64;            // 64-wide slices of D
+  static constexpr int kPanelBytes = 128 * 128;     // 128 rows x 128 bytes, of Q, K or V
+  static constexpr int kBytes = kPanels * kPanelBytes;  // one Q, K or V tile
+  static constexpr int q_off = 0;                   // two Q tiles (the two halves)
+  static constexpr int k_off = q_off + 2 * kBytes;
+  static constexpr int v_off = k_off + kStages * kBytes;
+  static constexpr int bar_off = v_off + kStages * kBytes;
+  static constexpr int used = bar_off + 256;
+  // one CTA per SM (its tensor memory is all of the SM's)
+  static constexpr int total = (used < 120 * 1024 ? 120 * 1024 : used) + 1024;
+  static_assert(total <= 227 * 1024, "shared memory of one CTA");
+};
+
+// mbarrier indices
+enum : int {
+  kBarQFull = 0,                    // the bf16 Q tiles have arrived
+  kBarQReady,                       // and are f16
+  kBarQEmpty,
+  kBarKFull,                        // + stage
+  kBarKEmpty = kBarKFull + kStages,
+  kBarVFull = kBarKEmpty + kStages,
+  kBarVEmpty = kBarVFull + kStages,
+  kBarSFull = kBarVEmpty + kStages,  // + half
+  kBarPFull = kBarSFull + 2,
+  kBarODone = kBarPFull + 2,
+  kNumBars = kBarODone + 2
+};
+static_assert(kNumBars * 8 <= 256, "barriers must fit their 256-byte area");
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// The eight codes of a word times `scale`, as one 16-byte unit of a swizzled tile
+__device__ __forceinline__ void store_unit(uint32_t addr, uint32_t word, __half2 scale) {
+  __half2 x[4];
+  e2m1x8_to_half2(word, x);
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 y = __hmul2(x[i], scale);
+    r[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+// One lane's share of the K or the V of a cache block: 16 / 8 bytes of codes
+// twice, with their scales.  V's two halves hold two tokens each.
+template <int D>
+struct Share {
+  uint32_t w[2][D / 32];
+  uint32_t s[2];  // two scale bytes each
+  // `tile`: the block's, or null (zeros)
+  __device__ __forceinline__ void load_k(const uint8_t* tile, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s[i] = 0;
+      if constexpr (D == 128) {  // 16 bytes of token 8 i + lane / 4
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (tile) {
+          v = *(const uint4*)(tile + (i * 32 + lane) * 16);
+          s[i] = *(const uint16_t*)(tile + Fp4Tile<D>::ks_off + (i * 32 + lane) * 2);
+        }
+        w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+      } else {  // 8 bytes of token 8 i + lane / 4, one scale
+        uint2 v = make_uint2(0, 0);
+        if (tile) {
+          v = *(const uint2*)(tile + (i * 32 + lane) * 8);
+          s[i] = tile[Fp4Tile<D>::ks_off + i * 32 + lane];
+        }
+        w[i][0] = v.x; w[i][1] = v.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void load_v(const uint8_t* tile, int lane) {
+    const int c = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s[i] = 0;
+      if constexpr (D == 128) {  // tokens 4 t + 2 i, + 1: 8 bytes each
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (tile) {
+          v = *(const uint4*)(tile + Fp4Tile<D>::v_off + (i * 32 + lane) * 16);
+          s[i] = *(const uint16_t*)(tile + Fp4Tile<D>::vs_off + c * 16 + 4 * t + 2 * i);
+        }
+        w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+      } else {  // 4 bytes each
+        uint2 v = make_uint2(0, 0);
+        if (tile) {
+          v = *(const uint2*)(tile + Fp4Tile<D>::v_off + (i * 32 + lane) * 8);
+          s[i] = *(const uint16_t*)(tile + Fp4Tile<D>::vs_off + (c >> 1) * 16 + 4 * t + 2 * i);
+        }
+        w[i][0] = v.x; w[i][1] = v.y;
+      }
+    }
+  }
+  // Rows row0 .. row0 + 15 of a K / V tile at `dst`; of tokens from `held` on,
+  // zeros.  The order of a lane's stores keeps the eight lanes of a phase on
+  // different banks.
+  __device__ __forceinline__ void store_k(uint32_t dst, int row0, int held, int lane) const {
+    const int c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int token = 8 * i + (lane >> 2), row = row0 + token;
+      const __half2 two = e4m3x2_to_half2(token < held ? s[i] : 0u);
+      const __half2 lo = __low2half2(two), hi = D == 128 ? __high2half2(two) : lo;
+      if constexpr (D == 128) {  // dims 32 c ..: panel c / 2, units 4 (c % 2) ..
+        const uint32_t line = dst + (c >> 1) * Layout<D>::kPanelBytes + row * 128;
+        const int turn = c & 2;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int u = j ^ turn;  // (0, 1, 2, 3) or (2, 3, 0, 1)
+          const uint32_t word = turn ? w[i][j ^ 2] : w[i][j];
+          store_unit(line + ((((c & 1) * 4 + u) ^ (row & 7)) << 4), word, u < 2 ? lo : hi);
+        }
+      } else {  // dims 16 c ..: units 2 c, 2 c + 1
+        const uint32_t line = dst + row * 128;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          store_unit(line + (((2 * c + j) ^ (row & 7)) << 4), w[i][j], lo);
+      }
+    }
+  }
+  __device__ __forceinline__ void store_v(uint32_t dst, int row0, int held, int lane) const {
+    const int c = lane >> 2, t = lane & 3;
+    const int turn = t >> 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int token = 4 * t + 2 * i;
+      uint32_t two = s[i];
+      if (token + 1 >= held) two = token >= held ? 0u : two & 0xffu;
+      const __half2 sc = e4m3x2_to_half2(two);
+      const __half2 s0 = __low2half2(sc), s1 = __high2half2(sc);
+      if constexpr (D == 128) {  // dims 16 c ..: panel c / 4, units 2 (c % 4), + 1
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = j >> 1, row = row0 + token + k;   // token of the pair
+          const int h = (j & 1) ^ turn;
+          const uint32_t word = turn ? w[i][2 * k + (~j & 1)] : w[i][j];
+          store_unit(dst + (c >> 2) * Layout<D>::kPanelBytes + row * 128 +
+                         (((2 * (c & 3) + h) ^ (row & 7)) << 4),
+                     word, k ? s1 : s0);
+        }
+      } else {  // dims 8 c ..: unit c
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int k = j ^ turn, row = row0 + token + k;
+          const uint32_t word = turn ? w[i][j ^ 1] : w[i][j];
+          store_unit(dst + row * 128 + ((c ^ (row & 7)) << 4), word, k ? s1 : s0);
+        }
+      }
+    }
+  }
+};
+
+// The tiles of a CTA's items one after the other, as the producers walk them
+struct TileCursor {
+  int k = -1, t = 0, ntiles = 0;  // item of this CTA, tile in it
+  int kvh, L, nblk;
+  const int32_t* table;
+  bool done = false;
+  __device__ __forceinline__ void next(const AttnParams& p, const PrefillWork& work, int num_items) {
+    if (done) return;
+    while (++t >= ntiles) {
+      const int w = item_index(++k);
+      if (w >= num_items) {
+        done = true;
+        return;
+      }
+      const ItemInfo it = load_item(p, work, w);
+      t = -1;
+      ntiles = it.ntiles;
+      kvh = it.head0 / p.group;
+      L = it.L;
+      nblk = (it.L + kBlockSize - 1) / kBlockSize;
+      table = p.block_tables + (int64_t)it.seq * p.max_blocks_per_seq;
+    }
+  }
+  // lane b < 8: the id of the tile's block b, or -1 (past the sequence, or
+  // outside the pool)
+  __device__ __forceinline__ int ids(const AttnParams& p, int lane) const {
+    const int b = t * kTileBlocks + lane;
+    int id = -1;
+    if (!done && lane < kTileBlocks && b < nblk && b < p.max_blocks_per_seq) id = table[b];
+    return id < p.num_blocks ? id : -1;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constant__ CUtensorMap tm_q,
+                   int pair_heads, const __grid_constant__ PrefillWork work) {
+  using LY = Layout<D>;
+  constexpr int kPanels = LY::kPanels;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint32_t sh_tmem_base;
+  __shared__ int sh_abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = ((uint32_t)__cvta_generic_to_shared(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sQ = base + LY::q_off, sK = base + LY::k_off, sV = base + LY::v_off,
+                 sBar = base + LY::bar_off;
+  auto bar = [&](int i) { return sBar + 8u * (uint32_t)i; };
+  volatile int* abort_flag = &sh_abort;
+
+  if (threadIdx.x == 0) {
+    sh_abort = 0;
+    mbar_init(bar(kBarQFull), 1);
+    mbar_init(bar(kBarQReady), 8);  // one arrival per softmax warp
+    mbar_init(bar(kBarQEmpty), 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(kBarKFull + i), kProducers);
+      mbar_init(bar(kBarKEmpty + i), 1);
+      mbar_init(bar(kBarVFull + i), kProducers);
+      mbar_init(bar(kBarVEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarSFull + i), 1);
+      mbar_init(bar(kBarPFull + i), 4);  // one arrival per softmax warp of the half
+      mbar_init(bar(kBarODone + i), 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tmap(&tm_q);
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc((uint32_t)__cvta_generic_to_shared(&sh_tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh_tmem_base;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int num_items = work.count > 0 ? work.count : p.ws_items[0].x;
+  int* status = p.ws_status;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp != kWarpMma) {
+      // ============ producers: K and V tiles from codes; warp 8 the Q tiles too ============
+      // A phase is the K or the V of a tile.  A warp takes three (or two) of
+      // the phase's blocks, every third; the codes of the phase after are
+      // loaded as each block of this one has been stored.
+      const int me = warp == kWarpQ ? 0 : warp - 9;   // 0, 1, 2
+      const int k0 = me, v0 = 2 - me;                 // its first block of a K / V phase
+      const uint8_t* cache = (const uint8_t*)p.k_cache;
+      TileCursor cur, nxt;
+      nxt.next(p, work, num_items);
+      int ids_n = nxt.ids(p, lane);
+      auto tile_of = [&](int ids, int b, int kvh) -> const uint8_t* {
+        const int id = __shfl_sync(0xffffffffu, ids, b & 7);
+        return b < kTileBlocks && id >= 0
+                   ? cache + ((int64_t)id * p.num_kv_heads + kvh) * Fp4Tile<D>::bytes
+                   : nullptr;
+      };
+      Share<D> sh[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) sh[i].load_k(tile_of(ids_n, k0 + 3 * i, nxt.kvh), lane);
+      uint32_t g = 0;  // global tile counter
+      bool ok = true;
+      int item = -1;
+      while (!nxt.done && ok) {
+        cur = nxt;
+        const int ids = ids_n;
+        if (warp == kWarpQ && cur.k != item) {
+          // ---- the item's two Q tiles
+          item = cur.k;
+          if (lane == 0) {
+            if (item > 0) ok = wait_bar(bar(kBarQEmpty), (item - 1) & 1, abort_flag, status);
+            if (ok) {
+              const ItemInfo it = load_item(p, work, item_index(item));
+              mbar_expect_tx(bar(kBarQFull), 2 * LY::kBytes);
+              for (int h = 0; h < 2; ++h) {
+                const int head = pair_heads ? it.head0 + h : it.head0;
+                const int qt = pair_heads ? it.qt0 : it.qt0 + h;
+                for (int pn = 0; pn < kPanels; ++pn)
+                  tma_load_3d(sQ + h * LY::kBytes + pn * LY::kPanelBytes, &tm_q, 64 * pn, head,
+                              it.q0 + qt * QT, bar(kBarQFull));
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+        }
+        nxt.next(p, work, num_items);
+        ids_n = nxt.ids(p, lane);
+        const int st = g % kStages;
+        const int key0 = cur.t * KT;
+#pragma unroll
+        for (int phase = 0; phase < 2 && ok; ++phase) {
+          const int full = (phase ? kBarVFull : kBarKFull) + st;
+          const int empty = (phase ? kBarVEmpty : kBarKEmpty) + st;
+          if (g >= kStages) {
+            ok = wait_bar(bar(empty), ((g / kStages) - 1) & 1, abort_flag, status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          const uint32_t dst = (phase ? sV : sK) + st * LY::kBytes;
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const int b = (phase ? v0 : k0) + 3 * i;
+            if (b < kTileBlocks) {
+              const int held = cur.L - key0 - b * kBlockSize;  // tokens of the block
+              if (phase)
+                sh[i].store_v(dst, b * kBlockSize, held, lane);
+              else
+                sh[i].store_k(dst, b * kBlockSize, held, lane);
+            }
+            // the same slot of the next phase: this tile's V, the next one's K
+            if (phase)
+              sh[i].load_k(tile_of(ids_n, k0 + 3 * i, nxt.kvh), lane);
+            else
+              sh[i].load_v(tile_of(ids, v0 + 3 * i, cur.kvh), lane);
+          }
+          fence_proxy_async_smem();  // the stores, before the tensor core reads them
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(full));
+        }
+        ++g;
+      }
+    } else {
+      // =========================== MMA issuer ===========================
+      // (as in the bf16 kernel: P.V of tile g-1 before Q K^T of tile g, per half)
+      constexpr uint32_t idesc_qk = instr_desc(128, KT, 0, 0, 0);
+      constexpr uint32_t idesc_pv = instr_desc(128, D, 0, 1, 0);
+      const uint64_t dq0 = smem_desc(sQ, 16, 1024);
+      const uint64_t dk0 = smem_desc(sK, 16, 1024);
+      const uint64_t dv0 = smem_desc(sV, LY::kPanelBytes, 1024);
+      uint32_t g = 0;
+      bool ok = true;
+      auto issue_pv = [&](int h, uint32_t gt, bool first_of_item) {  // O_h += P_h V (tile gt)
+        ok = wait_bar(bar(kBarPFull + h), gt & 1, abort_flag, status);
+        if (!ok) return;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t dv = dv0 + (uint64_t)(((gt % kStages) * LY::kBytes) >> 4);
+          const uint32_t dst = tmem + kTmemO + 128 * h;
+          const uint32_t pa = tmem + kTmemS + 128 * h;
+#pragma unroll
+          for (int kk = 0; kk < KT / 16; ++kk)
+            umma_bf16_ts(dst, pa + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                         (first_of_item && kk == 0) ? 0u : 1u);
+          umma_commit(bar(kBarODone + h));
+        }
+        __syncwarp();
+      };
+      auto issue_qk = [&](int h, uint32_t gt) {  // S_h = Q_h K^T (tile gt)
+        if (lane == 0) {
+          const uint64_t dk = dk0 + (uint64_t)(((gt % kStages) * LY::kBytes) >> 4);
+          const uint64_t dq = dq0 + (uint64_t)((h * LY::kBytes) >> 4);
+          const uint32_t dst = tmem + kTmemS + 128 * h;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = ((kk / 4) * LY::kPanelBytes + (kk % 4) * 32) >> 4;
+            umma_bf16(dst, dq + o, dk + o, idesc_qk, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(bar(kBarSFull + h));
+        }
+        __syncwarp();
+      };
+      for (int k = 0; ok; ++k) {
+        const int w = item_index(k);
+        if (w >= num_items) break;
+        const ItemInfo it = load_item(p, work, w);
+        ok = wait_bar(bar(kBarQReady), k & 1, abort_flag, status);
+        const uint32_t g_first = g;
+        for (int t = 0; t < it.ntiles && ok; ++t, ++g) {
+          ok = wait_bar(bar(kBarKFull + g % kStages), (g / kStages) & 1, abort_flag, status);
+          if (ok && t > 0)
+            ok = wait_bar(bar(kBarVFull + (g - 1) % kStages), ((g - 1) / kStages) & 1, abort_flag,
+                          status);
+          if (!ok) break;
+          tc_fence_after();
+          for (int h = 0; h < 2 && ok; ++h) {
+            if (t > 0) issue_pv(h, g - 1, g - 1 == g_first);  // P_h of the previous tile
+            if (ok) issue_qk(h, g);
+          }
+          if (ok && lane == 0) {
+            umma_commit(bar(kBarKEmpty + g % kStages));
+            if (t > 0) umma_commit(bar(kBarVEmpty + (g - 1) % kStages));
+            if (t == it.ntiles - 1) umma_commit(bar(kBarQEmpty));
+          }
+          __syncwarp();
+        }
+        if (ok && it.ntiles > 0) {  // P.V of the item's last tile
+          const uint32_t gl = g - 1;
+          ok = wait_bar(bar(kBarVFull + gl % kStages), (gl / kStages) & 1, abort_flag, status);
+          if (ok) tc_fence_after();
+          for (int h = 0; h < 2 && ok; ++h) issue_pv(h, gl, gl == g_first);
+          if (ok && lane == 0) umma_commit(bar(kBarVEmpty + gl % kStages));
+          __syncwarp();
+        }
+      }
+    }
+  } else {
+    // =========================== softmax (two halves) ===========================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int h = warp >> 2;                   // which Q tile
+    const int quarter = warp & 3;              // TMEM lanes 32*quarter .. +31
+    const int row = quarter * 32 + lane;       // query row of this thread in its tile
+    const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_addr + kTmemS + 128 * h;
+    const uint32_t tO = tmem + lane_addr + kTmemO + 128 * h;
+    uint32_t g = 0;
+    bool ok = true;
+    // this row of item k's Q from bf16 to f16 in place, times 2^-e (e: the
+    // exponent of its largest value; two factors, since 2^127 and 2^-128 alone
+    // are no normal fp32 numbers); sets the scale of the row's scores
+    float sl2_next = 0.f;
+    auto convert_q = [&](int k) {
+      ok = wait_bar(bar(kBarQFull), k & 1, abort_flag, status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      uint32_t q[D / 2];
+      const uint32_t line = sQ + h * LY::kBytes + row * 128;
+#pragma unroll
+      for (int u = 0; u < D / 8; ++u)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q[4 * u]), "=r"(q[4 * u + 1]), "=r"(q[4 * u + 2]), "=r"(q[4 * u + 3])
+                     : "r"(line + (u / 8) * LY::kPanelBytes + (((u % 8) ^ (row & 7)) << 4)));
+      uint32_t top = 0;  // the largest magnitude's bits (bf16 order is that of its bits)
+#pragma unroll
+      for (int i = 0; i < D / 2; ++i)
+        top = max(top, max(q[i] & 0x7fffu, q[i] >> 16 & 0x7fffu));
+      const int e = (int)(top >> 7) - 127, e1 = e / 2;
+      const float f1 = exp2i(-e1), f2 = exp2i(e1 - e);
+      sl2_next = p.scale_log2 * exp2i(e1) * exp2i(e - e1);
+#pragma unroll
+      for (int u = 0; u < D / 8; ++u) {
+#pragma unroll
+        for (int i = 4 * u; i < 4 * u + 4; ++i)
+          q[i] = pack_f16x2(__uint_as_float(q[i] << 16) * f1 * f2,
+                            __uint_as_float(q[i] & 0xffff0000u) * f1 * f2);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         line + (u / 8) * LY::kPanelBytes + (((u % 8) ^ (row & 7)) << 4)),
+                     "r"(q[4 * u]), "r"(q[4 * u + 1]), "r"(q[4 * u + 2]), "r"(q[4 * u + 3])
+                     : "memory");
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarQReady));
+    };
+    if (item_index(0) < num_items) convert_q(0);
+    for (int k = 0; ok; ++k) {
+      const int w = item_index(k);
+      if (w >= num_items) break;
+      const ItemInfo it = load_item(p, work, w);
+      const int head = pair_heads ? it.head0 + h : it.head0;
+      const int qt = pair_heads ? it.qt0 : it.qt0 + h;
+      const int jq = qt * QT + row;
+      const bool row_valid = jq < it.ql;
+      const int pos = row_valid ? it.L - it.ql + jq : -1;  // last visible key
+      const int min_pos = it.L - it.ql + qt * QT;          // smallest position in the tile
+      const float sl2 = sl2_next;
+      float m_run = -INFINITY, l_run = 0.f;
+      const uint32_t g_first = g;
+      for (int t = 0; t < it.ntiles && ok; ++t, ++g) {
+        // S_h of tile g is complete; so is P.V of tile g-1 (issued before it)
+        ok = wait_bar(bar(kBarSFull + h), g & 1, abort_flag, status);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[KT];
+        tmem_ld32_at<0>(tS, sr);
+        tmem_ld32_at<32>(tS + 32, sr);
+        tmem_ld32_at<64>(tS + 64, sr);
+        tmem_ld32_at<96>(tS + 96, sr);
+        tmem_ld_wait();
+        float s[KT];
+#pragma unroll
+        for (int n = 0; n < KT; ++n) s[n] = __uint_as_float(sr[n]);
+        // ---- keys past this row's last visible one are out
+        if (t * KT + KT - 1 > min_pos) {
+          const int lim = pos - t * KT;
+#pragma unroll
+          for (int n = 0; n < KT; ++n) s[n] = n <= lim ? s[n] : -INFINITY;
+        }
+        // ---- row max of the raw scores: kMaxChains independent chains of
+        // three-input maxima, then a tree
+        float mc[kMaxChains];
+#pragma unroll
+        for (int q = 0; q < kMaxChains; ++q) mc[q] = fmaxf(s[2 * q], s[2 * q + 1]);
+#pragma unroll
+        for (int n = 2 * kMaxChains; n < KT; n += 2 * kMaxChains) {
+#pragma unroll
+          for (int q = 0; q < kMaxChains; ++q) mc[q] = max3(mc[q], s[n + 2 * q], s[n + 2 * q + 1]);
+        }
+#pragma unroll
+        for (int c = kMaxChains; c > 1; c /= 2) {
+#pragma unroll
+          for (int q = 0; q < c / 2; ++q) mc[q] = fmaxf(mc[q], mc[q + c / 2]);
+        }
+        const float mx = sl2 * mc[0];
+        // ---- running max (log2 units): moved only when it grows past the threshold
+        float alpha = 1.f;
+        if (mx > m_run + kRescaleThreshold || (m_run == -INFINITY && mx > -INFINITY)) {
+          alpha = (m_run == -INFINITY) ? 0.f : ex2(m_run - mx);
+          m_run = mx;
+        }
+        const float neg_base = (m_run == -INFINITY) ? 0.f : kPShift - m_run;
+        // ---- P = 2^7 exp2(S * scale * log2(e) - max) on pairs of columns; two
+        // f16 per word, written over the first half of S
+        const uint64_t scale2 = f2(sl2, sl2), base2 = f2(neg_base, neg_base);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pw[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int n = 64 * c + 2 * j;
+            const uint64_t x = fma2(f2(s[n], s[n + 1]), scale2, base2);
+            float x0, x1;
+            f2_split(x, x0, x1);
+            const uint64_t e = f2(ex2(x0), ex2(x1));  // masked: ex2(-inf) = 0
+            acc[j & 3] = add2(acc[j & 3], e);
+            float e0, e1;
+            f2_split(e, e0, e1);
+            pw[j] = pack_f16x2(e0, e1);
+          }
+          tmem_st32(tS + 32 * c, pw);
+        }
+        float sum;
+        {
+          float a0, a1;
+          f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), a0, a1);
+          sum = a0 + a1;
+        }
+        l_run = l_run * alpha + sum;
+        // ---- O carries the old max: rescale it (P.V of tile g-1 is complete)
+        if (g != g_first && __any_sync(0xffffffffu, alpha != 1.f)) {
+          const uint64_t alpha2 = f2(alpha, alpha);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t orr[32];
+            tmem_ld32(tO + c * 32, orr);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              uint32_t lo, hi;
+              u2_split(mul2(u2(orr[2 * e], orr[2 * e + 1]), alpha2), lo, hi);
+              orr[2 * e] = lo;
+              orr[2 * e + 1] = hi;
+            }
+            tmem_st32(tO + c * 32, orr);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPFull + h));
+      }
+      // the next item's Q while this one's last P.V runs
+      if (ok && item_index(k + 1) < num_items) convert_q(k + 1);
+      if (!ok || it.ntiles == 0) continue;
+      // ---- epilogue: O / l to global memory
+      ok = wait_bar(bar(kBarODone + h), (g - 1) & 1, abort_flag, status);
+      if (!ok) break;
+      tc_fence_after();
+      const float inv = v_scale / l_run;
+      __nv_bfloat16* orow =
+          (__nv_bfloat16*)p.out + ((int64_t)(it.q0 + jq) * p.num_q_heads + head) * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t orr[32];
+        tmem_ld32(tO + c * 32, orr);
+        tmem_ld_wait();
+        if (row_valid) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint4 pk;
+            pk.x = pack_bf16x2(__uint_as_float(orr[8 * v + 0]) * inv, __uint_as_float(orr[8 * v + 1]) * inv);
+            pk.y = pack_bf16x2(__uint_as_float(orr[8 * v + 2]) * inv, __uint_as_float(orr[8 * v + 3]) * inv);
+            pk.z = pack_bf16x2(__uint_as_float(orr[8 * v + 4]) * inv, __uint_as_float(orr[8 * v + 5]) * inv);
+            pk.w = pack_bf16x2(__uint_as_float(orr[8 * v + 6]) * inv, __uint_as_float(orr[8 * v + 7]) * inv);
+            *reinterpret_cast<uint4*>(orow + c * 32 + 8 * v) = pk;
+          }
+        }
+      }
+      // the next item's first P.V overwrites O: every lane has read it
+      tc_fence_before();
+    }
+  }
+
+  // ---- wind down: every role is done (or gave up); free TMEM
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const AttnParams& p, float v_scale, int max_query_len,
+                     const int32_t* seq_lens_host, const int32_t* query_start_loc_host,
+                     cudaStream_t stream) {
+  CUtensorMap tq;
+  if (!make_map(&tq, p.q, D, p.num_q_heads, p.num_tokens, (uint64_t)D * 2,
+                (uint64_t)p.num_q_heads * D * 2, 1, QT))
+    return cudaErrorInvalidValue;
+  const int pair_heads = (p.group % 2 == 0) ? 1 : 0;
+  static thread_local PrefillWork work;  // 16 KB: kept off the stack
+  int upper = 0;
+  cudaError_t e = prefill_work_list(&work, &upper, p, max_query_len, -1, seq_lens_host,
+                                    query_start_loc_host, pair_heads, stream);
+  if (e != cudaSuccess) return e;
+  auto kernel = prefill_fp4_kernel<D>;
+  const int smem = Layout<D>::total;
+  static std::atomic<int> smem_done[64];
+  e = raise_smem_limit(kernel, smem, smem_done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(max(1, min(device_sm_count(), upper)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, v_scale, tq, pair_heads, work);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_fp4(const AttnParams& p, float v_scale, int head_dim,
+                               int max_query_len, const int32_t* seq_lens_host,
+                               const int32_t* query_start_loc_host, cudaStream_t stream) {
+  cudaError_t e = head_dim == 64
+                      ? launch_d<64>(p, v_scale, max_query_len, seq_lens_host,
+                                     query_start_loc_host, stream)
+                      : launch_d<128>(p, v_scale, max_query_len, seq_lens_host,
+                                      query_start_loc_host, stream);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace pa

@@ -43,14 +43,14 @@
 
 #include "pa_fastmath.cuh"
 #include "pa_internal.cuh"
+#include "pa_prefill_plan.cuh"
+#include "pa_tcgen05.cuh"
 #include "pa_tma.cuh"
 #include "pa_wait.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int QT = kPrefillQTile;               // 128 query rows per Q tile
-constexpr int KT = kPrefillKvTile;              // 128 keys per K/V tile
 constexpr int kTileBlocks = KT / kBlockSize;    // 8 cache blocks per tile
 // K / V tile stages: a K tile is needed one MMA round after V's (P.V of a
 // tile follows its Q K^T), so K benefits first from a deeper ring
@@ -112,154 +112,6 @@ enum : int {
   kNumBars = kBarODone + 2
 };
 static_assert(kNumBars * 8 <= 256, "barriers must fit their 256-byte area");
-
-// ------------------------------------------------------------------ PTX wrappers
-
-__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
-               "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// the same, with A (M x 16, bf16 packed two per 32-bit column) read from TMEM
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                             uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-
-#define PA_R32(r)                                                                           \
-  "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),       \
-      "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), \
-      "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),          \
-      "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),          \
-      "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-#define PA_W32(r)                                                                          \
-  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),   \
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),      \
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),    \
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),    \
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
-
-// 32 consecutive fp32 columns of this thread's TMEM lane
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : PA_R32(r)
-      : "r"(taddr));
-}
-// 32 consecutive fp32 columns into elements OFF .. OFF+31 of a larger array
-template <int OFF, int N>
-__device__ __forceinline__ void tmem_ld32_at(uint32_t taddr, uint32_t (&r)[N]) {
-  static_assert(OFF + 32 <= N, "tmem_ld32_at out of range");
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[OFF + 0]), "=r"(r[OFF + 1]), "=r"(r[OFF + 2]), "=r"(r[OFF + 3]),
-        "=r"(r[OFF + 4]), "=r"(r[OFF + 5]), "=r"(r[OFF + 6]), "=r"(r[OFF + 7]),
-        "=r"(r[OFF + 8]), "=r"(r[OFF + 9]), "=r"(r[OFF + 10]), "=r"(r[OFF + 11]),
-        "=r"(r[OFF + 12]), "=r"(r[OFF + 13]), "=r"(r[OFF + 14]), "=r"(r[OFF + 15]),
-        "=r"(r[OFF + 16]), "=r"(r[OFF + 17]), "=r"(r[OFF + 18]), "=r"(r[OFF + 19]),
-        "=r"(r[OFF + 20]), "=r"(r[OFF + 21]), "=r"(r[OFF + 22]), "=r"(r[OFF + 23]),
-        "=r"(r[OFF + 24]), "=r"(r[OFF + 25]), "=r"(r[OFF + 26]), "=r"(r[OFF + 27]),
-        "=r"(r[OFF + 28]), "=r"(r[OFF + 29]), "=r"(r[OFF + 30]), "=r"(r[OFF + 31])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(
-          taddr),
-      PA_W32(r)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld_wait() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// Shared-memory matrix descriptor (tcgen05): 128-byte swizzle, start address,
-// leading / stride byte offsets (all in 16-byte units), descriptor version 1.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// Instruction descriptor of kind::f16 with bf16 operands and an fp32 accumulator.
-__host__ __device__ constexpr uint32_t instr_desc(int M, int N, int a_mn_major, int b_mn_major) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn_major << 15) |
-         ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// A work item is two 128-row Q tiles that read the same keys: two q-heads of
-// one kv-head (pair_heads), or two consecutive query tiles of one q-head.
-struct ItemInfo {
-  int seq, qt0, head0, ntiles;
-  int q0, ql, L;
-};
-
-// A work list the host built from its copies of the step's lengths, passed as
-// a kernel parameter (count 0: the list is in the workspace, built by
-// prefill_plan_kernel).
-constexpr int kParamItems = 1024;
-struct PrefillWork {
-  int count;
-  int pad[3];
-  int4 items[kParamItems];
-};
-
-__device__ __forceinline__ ItemInfo load_item(const AttnParams& p, const PrefillWork& work,
-                                              int w) {
-  const int4 it = work.count > 0 ? work.items[w] : p.ws_items[1 + w];
-  ItemInfo r;
-  r.seq = it.x; r.qt0 = it.y; r.head0 = it.z; r.ntiles = it.w;
-  r.q0 = p.query_start_loc[r.seq];
-  r.ql = p.query_start_loc[r.seq + 1] - r.q0;
-  r.L = p.seq_lens[r.seq];
-  return r;
-}
-
-// item index of the k-th item of CTA c (boustrophedon over rounds of gridDim)
-__device__ __forceinline__ int item_index(int k) {
-  const int g = gridDim.x, c = blockIdx.x;
-  return k * g + ((k & 1) ? (g - 1 - c) : c);
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -634,117 +486,7 @@ prefill_tcgen05_kernel(const AttnParams p, const __grid_constant__ CUtensorMap t
   }
 }
 
-// --------------------------------------------------------------- work list
-
-// One CTA: list the prefill items of every sequence with q_len * group > 64,
-// heaviest (most key tiles) first (a counting sort on the tile count), and
-// store the count in ws_items[0].x.  An item pairs two q-heads of one kv-head
-// (pair_heads: the group is even) or two consecutive query tiles of one
-// q-head; its tile count covers the later of its two query tiles.
-__host__ __device__ __forceinline__ void prefill_item_range(int L, int ql, int pair_heads,
-                                                            int i, int* last_row_pos) {
-  const int hi_tile = pair_heads ? i : 2 * i + 1;
-  const int last_row = min((hi_tile + 1) * QT, ql) - 1;
-  *last_row_pos = L - ql + last_row;
-}
-
-__global__ void __launch_bounds__(1024)
-prefill_plan_kernel(const AttnParams p, int max_tiles, int pair_heads) {
-  extern __shared__ int hist[];  // [max_tiles + 1] counters, then running offsets
-  // the prefill kernel may be launched at once: it waits for this grid before
-  // it reads the work list
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int i = threadIdx.x; i <= max_tiles; i += blockDim.x) hist[i] = 0;
-  __syncthreads();
-  const int per_tile = pair_heads ? p.num_q_heads / 2 : p.num_q_heads;  // items per (seq, tile)
-  // pass 1: histogram of items by tile count
-  for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
-    const int q0 = p.query_start_loc[s], ql = p.query_start_loc[s + 1] - q0, L = p.seq_lens[s];
-    if (ql * p.group <= kDecodeMaxRows || ql > L) continue;
-    const int nq = (ql + QT - 1) / QT;
-    const int ni = pair_heads ? nq : (nq + 1) / 2;
-    for (int i = 0; i < ni; ++i) {
-      int last;
-      prefill_item_range(L, ql, pair_heads, i, &last);
-      const int nt = min(last / KT + 1, max_tiles);
-      atomicAdd(&hist[nt], per_tile);
-    }
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {  // exclusive offsets, descending tile count
-    int run = 0;
-    for (int nt = max_tiles; nt >= 0; --nt) {
-      const int c = hist[nt];
-      hist[nt] = run;
-      run += c;
-    }
-    p.ws_items[0] = make_int4(min(run, p.max_items), 0, 0, 0);
-  }
-  __syncthreads();
-  // pass 2: scatter
-  for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
-    const int q0 = p.query_start_loc[s], ql = p.query_start_loc[s + 1] - q0, L = p.seq_lens[s];
-    if (ql * p.group <= kDecodeMaxRows || ql > L) continue;
-    const int nq = (ql + QT - 1) / QT;
-    const int ni = pair_heads ? nq : (nq + 1) / 2;
-    for (int i = ni - 1; i >= 0; --i) {
-      int last;
-      prefill_item_range(L, ql, pair_heads, i, &last);
-      const int nt = min(last / KT + 1, max_tiles);
-      const int at = atomicAdd(&hist[nt], per_tile);
-      for (int h = 0; h < per_tile; ++h) {
-        if (at + h >= p.max_items) break;
-        p.ws_items[1 + at + h] = pair_heads ? make_int4(s, i, 2 * h, nt)
-                                            : make_int4(s, 2 * i, h, nt);
-      }
-    }
-  }
-}
-
 // ------------------------------------------------------------------ host side
-
-// The work list of prefill_plan_kernel, built on the host from its copies of
-// the step's lengths: the same items, heaviest first.  False when there are
-// more items than a kernel parameter holds.
-bool host_work_list(PrefillWork* work, const AttnParams& p, const int32_t* seq_lens_host,
-                    const int32_t* query_start_loc_host, int max_tiles, int pair_heads) {
-  const int per_tile = pair_heads ? p.num_q_heads / 2 : p.num_q_heads;
-  static thread_local int hist[1 << 16];
-  if (max_tiles + 1 > (1 << 16)) return false;
-  for (int i = 0; i <= max_tiles; ++i) hist[i] = 0;
-  long total = 0;
-  auto for_each_item = [&](auto fn) {
-    for (int s = 0; s < p.num_seqs; ++s) {
-      const int ql = query_start_loc_host[s + 1] - query_start_loc_host[s];
-      const int L = seq_lens_host[s];
-      if (ql * p.group <= kDecodeMaxRows || ql > L) continue;
-      const int nq = (ql + QT - 1) / QT;
-      const int ni = pair_heads ? nq : (nq + 1) / 2;
-      for (int i = 0; i < ni; ++i) {
-        int last;
-        prefill_item_range(L, ql, pair_heads, i, &last);
-        fn(s, i, min(last / KT + 1, max_tiles));
-      }
-    }
-  };
-  for_each_item([&](int, int, int nt) { hist[nt] += per_tile; total += per_tile; });
-  if (total > kParamItems || total > p.max_items) return false;
-  int run = 0;
-  for (int nt = max_tiles; nt >= 0; --nt) {
-    const int c = hist[nt];
-    hist[nt] = run;
-    run += c;
-  }
-  for_each_item([&](int s, int i, int nt) {
-    int at = hist[nt];
-    hist[nt] += per_tile;
-    for (int h = 0; h < per_tile; ++h, ++at)
-      work->items[at] = pair_heads ? make_int4(s, i, 2 * h, nt) : make_int4(s, 2 * i, h, nt);
-  });
-  work->count = (int)total;
-  return total > 0;
-}
 
 template <int D>
 cudaError_t launch_d(const AttnParams& p, int max_query_len, int num_items,
@@ -765,40 +507,16 @@ cudaError_t launch_d(const AttnParams& p, int max_query_len, int num_items,
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
 
-  // the work list: from the host copies when given and small enough, else
-  // built on the device
   static thread_local PrefillWork work;  // 16 KB: kept off the stack
-  const int tiles = (p.max_blocks_per_seq * kBlockSize + KT - 1) / KT;
-  work.count = 0;
-  if (!(seq_lens_host && query_start_loc_host &&
-        host_work_list(&work, p, seq_lens_host, query_start_loc_host, tiles, pair_heads))) {
-    work.count = 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(1024);
-    cfg.dynamicSmemBytes = (tiles + 1) * sizeof(int);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cfg.dynamicSmemBytes > 48 * 1024) {
-      static std::atomic<int> plan_smem_done[64];
-      cudaError_t e = raise_smem_limit(prefill_plan_kernel, (int)cfg.dynamicSmemBytes,
-                                       plan_smem_done);
-      if (e != cudaSuccess) return e;
-    }
-    cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_plan_kernel, p, tiles, pair_heads);
-    if (e != cudaSuccess) return e;
-  }
-  const int upper = work.count > 0 ? work.count
-                  : num_items >= 0 ? num_items
-                                   : (int)min((long)p.max_items,
-                                              (long)p.num_seqs * ((max_query_len + QT - 1) / QT) *
-                                                  p.num_q_heads);
+  int upper = 0;
+  cudaError_t e = prefill_work_list(&work, &upper, p, max_query_len, num_items, seq_lens_host,
+                                    query_start_loc_host, pair_heads, stream);
+  if (e != cudaSuccess) return e;
   const int grid = max(1, min(min(device_sm_count(), max_ctas), upper));
   auto kernel = prefill_tcgen05_kernel<D>;
   const int smem = PrefillLayout<D>::total;
   static std::atomic<int> smem_done[64];
-  cudaError_t e = raise_smem_limit(kernel, smem, smem_done);
+  e = raise_smem_limit(kernel, smem, smem_done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
