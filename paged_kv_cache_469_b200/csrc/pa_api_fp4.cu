@@ -271,7 +271,7 @@ extern "C" int pa_attention_varlen_fp4(
   a.group = group;
   a.num_blocks = num_blocks;
   a.scale_log2 = p.scale_log2;
-  a.ws_status = p.ws_status;
+  a.ws_status = a.ws_header = p.ws_status;
   a.ws_items = (int4*)(ws + w.items_off);
   a.max_items = w.max_items;
   return launch_prefill_fp4(a, v_scale, head_dim, max_query_len, seq_lens_host,

@@ -10,19 +10,23 @@
 // 128-row Q tiles that read the same keys, 128 keys at a time, S and O in tensor
 // memory, P written back over S.  What differs is how the operands arrive:
 //
-//   warps 8, 10, 11  read the codes and scales of the tile's eight blocks one
+//   warps 8, 10 - 12, 14, 15  read the codes and scales of the tile's eight blocks one
 //               phase ahead into registers (4.5 bits a value: 18 KB a tile),
 //               convert them to f16 -- code * scale is exact there -- and store
 //               them as the 128-byte swizzled K and V tiles that tcgen05.mma
 //               reads; slots past the sequence are stored as zeros.  About 115
 //               instructions a lane and block, a third of a tile's MMA time,
 //               on issue slots that the softmax leaves free.
-//   warp 8      also loads the bf16 Q tiles by TMA
+//   warp 8      also loads the bf16 Q tiles by TMA, and takes the items
 //   warps 0..7  turn their query rows to f16 in place, each row times a power of
 //               two that brings its largest value into [1, 2) (bf16's bits fit),
 //               then run the softmax; P is f16, 2^7 times itself (at most 2^15),
 //               so that its small values keep their bits
 //   warp 9      MMA issuer
+//
+// A CTA's first item goes by its number, the others it takes from a counter as
+// the one before has two tiles left: the list is heaviest first, so the CTAs
+// end close together.
 //
 // Every mbarrier wait is bounded by a time limit; a wait that runs out sets a
 // status bit in the workspace and the CTA winds down instead of hanging.
@@ -42,12 +46,17 @@ namespace {
 
 constexpr int kTileBlocks = KT / kBlockSize;    // 8 cache blocks per tile
 constexpr int kStages = 2;                      // K tiles, and V tiles
-constexpr int kThreads = 384;                   // 12 warps = 3 warpgroups
-constexpr int kWarpQ = 8, kWarpMma = 9;
-constexpr int kProducers = 3;                   // warps 8, 10, 11
-// Registers: 2 x 128 x 208 + 128 x 88 = 384 x 168
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
-static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch,
+constexpr int kThreads = 512;                   // 16 warps = 4 warpgroups
+// Six producers: 8, 10, 11, 12, 14, 15.  Four chunks of 1024 over 2712 .. 5048
+// tokens: 358 us with three producers in 384 threads (a producer warp is bound
+// by its own latencies), 256 with six, 255 with seven, 247 with none of their
+// conversions.
+constexpr int kWarpQ = 8, kWarpMma = 9, kWarpIdle = 13;
+constexpr int kProducers = 6;
+// Registers: 2 x 128 x 192 + 2 x 128 x 64 = 512 x 128 (184 and 72: 276 us, the
+// softmax's row of scores no longer fits)
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 192, kRegsOther = 64;
+static_assert(2 * 128 * kRegsSoftmax + 256 * kRegsOther <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0, kTmemS = 256;    // + 128 * half
@@ -82,8 +91,10 @@ enum : int {
   kBarSFull = kBarVEmpty + kStages,  // + half
   kBarPFull = kBarSFull + 2,
   kBarODone = kBarPFull + 2,
-  kNumBars = kBarODone + 2
+  kBarItem = kBarODone + 2,          // + ring slot of items
+  kNumBars = kBarItem + 8
 };
+constexpr int kItemRing = 8;
 static_assert(kNumBars * 8 <= 256, "barriers must fit their 256-byte area");
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -107,109 +118,120 @@ __device__ __forceinline__ void store_unit(uint32_t addr, uint32_t word, __half2
                : "memory");
 }
 
-// One lane's share of the K or the V of a cache block: 16 / 8 bytes of codes
-// twice, with their scales.  V's two halves hold two tokens each.
+// One lane's share of the K or the V of a cache block: two pieces of codes, 16
+// bytes each at D = 128, 8 at D = 64, and their scales.
+//
+// A piece of K is 2 or 4 units (8 dims, 16 bytes of f16) of one token, a piece
+// of V that of two tokens.  The unit's place in a 128-byte swizzled tile is its
+// number xor the row's low three bits: with the lane's part of both in `at`, a
+// store takes one xor with a constant.  Lanes are dealt to pieces, and the
+// units of a V piece ordered by lane, so that the eight lanes that store at
+// once meet different banks.
 template <int D>
 struct Share {
   uint32_t w[2][D / 32];
-  uint32_t s[2];  // two scale bytes each
+  uint32_t s[2];
+
+  // K: piece `i` of a lane is token 8 i + token_k, chunk c of the row (D / 4
+  // dims, one or two scales)
+  static __device__ __forceinline__ int chunk_k(int lane) {
+    return D == 128 ? (lane & 1) | (lane >> 2 & 2) : lane & 3;
+  }
+  static __device__ __forceinline__ int token_k(int lane) {
+    return D == 128 ? (lane >> 1 & 3) | (lane >> 2 & 4) : lane >> 2;
+  }
+  // offset in a K tile of this lane's unit 0 in a block's first row of 8
+  static __device__ __forceinline__ uint32_t at_k(int lane) {
+    const int c = chunk_k(lane), token = token_k(lane);
+    return D == 128 ? (c >> 1) * Layout<D>::kPanelBytes + token * 128 +
+                          (((c & 1) * 4 ^ token) << 4)
+                    : token * 128 + ((2 * c ^ token) << 4);
+  }
+  // V: piece `i` is tokens 4 t + 2 i, + 1 of chunk c (D / 8 dims), c = lane / 4,
+  // t = lane % 4; lanes of t >= 2 store their odd units (at D = 64, their
+  // second piece) first
+  static __device__ __forceinline__ uint32_t at_v(int lane) {
+    const int c = lane >> 2, t = lane & 3;
+    return D == 128 ? (c >> 2) * Layout<D>::kPanelBytes + t * 512 +
+                          ((2 * (c & 3) ^ 4 * (t & 1) ^ t >> 1) << 4)
+                    : t * 512 + ((c ^ 4 * (t & 1)) << 4);
+  }
+
   // `tile`: the block's, or null (zeros)
   __device__ __forceinline__ void load_k(const uint8_t* tile, int lane) {
+    const int at = token_k(lane) * 4 + chunk_k(lane);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      s[i] = 0;
-      if constexpr (D == 128) {  // 16 bytes of token 8 i + lane / 4
+      if constexpr (D == 128) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (tile) {
-          v = *(const uint4*)(tile + (i * 32 + lane) * 16);
-          s[i] = *(const uint16_t*)(tile + Fp4Tile<D>::ks_off + (i * 32 + lane) * 2);
-        }
+        if (tile) v = *(const uint4*)(tile + i * 512 + at * 16);
+        s[i] = tile ? *(const uint16_t*)(tile + Fp4Tile<D>::ks_off + i * 64 + at * 2) : 0;
         w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
-      } else {  // 8 bytes of token 8 i + lane / 4, one scale
+      } else {
         uint2 v = make_uint2(0, 0);
-        if (tile) {
-          v = *(const uint2*)(tile + (i * 32 + lane) * 8);
-          s[i] = tile[Fp4Tile<D>::ks_off + i * 32 + lane];
-        }
+        if (tile) v = *(const uint2*)(tile + i * 256 + at * 8);
+        s[i] = tile ? tile[Fp4Tile<D>::ks_off + i * 32 + at] : 0;
         w[i][0] = v.x; w[i][1] = v.y;
       }
     }
   }
   __device__ __forceinline__ void load_v(const uint8_t* tile, int lane) {
     const int c = lane >> 2, t = lane & 3;
+    // the scales of tokens 4 t .. 4 t + 3
+    s[0] = tile ? *(const uint32_t*)(tile + Fp4Tile<D>::vs_off + (D == 128 ? c : c >> 1) * 16 +
+                                     4 * t)
+                : 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      s[i] = 0;
-      if constexpr (D == 128) {  // tokens 4 t + 2 i, + 1: 8 bytes each
+      if constexpr (D == 128) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (tile) {
-          v = *(const uint4*)(tile + Fp4Tile<D>::v_off + (i * 32 + lane) * 16);
-          s[i] = *(const uint16_t*)(tile + Fp4Tile<D>::vs_off + c * 16 + 4 * t + 2 * i);
-        }
+        if (tile) v = *(const uint4*)(tile + Fp4Tile<D>::v_off + i * 512 + lane * 16);
         w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
-      } else {  // 4 bytes each
+      } else {
         uint2 v = make_uint2(0, 0);
-        if (tile) {
-          v = *(const uint2*)(tile + Fp4Tile<D>::v_off + (i * 32 + lane) * 8);
-          s[i] = *(const uint16_t*)(tile + Fp4Tile<D>::vs_off + (c >> 1) * 16 + 4 * t + 2 * i);
-        }
+        if (tile) v = *(const uint2*)(tile + Fp4Tile<D>::v_off + i * 256 + lane * 8);
         w[i][0] = v.x; w[i][1] = v.y;
       }
     }
   }
-  // Rows row0 .. row0 + 15 of a K / V tile at `dst`; of tokens from `held` on,
-  // zeros.  The order of a lane's stores keeps the eight lanes of a phase on
-  // different banks.
-  __device__ __forceinline__ void store_k(uint32_t dst, int row0, int held, int lane) const {
-    const int c = lane & 3;
+  // Into the 16 rows at `at` (the block's first row's offset in the tile plus
+  // at_k / at_v); of tokens from `held` on, zeros.
+  __device__ __forceinline__ void store_k(uint32_t at, int held, int lane) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int token = 8 * i + (lane >> 2), row = row0 + token;
-      const __half2 two = e4m3x2_to_half2(token < held ? s[i] : 0u);
-      const __half2 lo = __low2half2(two), hi = D == 128 ? __high2half2(two) : lo;
-      if constexpr (D == 128) {  // dims 32 c ..: panel c / 2, units 4 (c % 2) ..
-        const uint32_t line = dst + (c >> 1) * Layout<D>::kPanelBytes + row * 128;
-        const int turn = c & 2;
+      const uint32_t bytes = 8 * i + token_k(lane) < held ? s[i] : 0u;
+      const __half2 two = e4m3x2_to_half2(bytes);
+      const __half2 lo = __low2half2(two), hi = __high2half2(two);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int u = j ^ turn;  // (0, 1, 2, 3) or (2, 3, 0, 1)
-          const uint32_t word = turn ? w[i][j ^ 2] : w[i][j];
-          store_unit(line + ((((c & 1) * 4 + u) ^ (row & 7)) << 4), word, u < 2 ? lo : hi);
-        }
-      } else {  // dims 16 c ..: units 2 c, 2 c + 1
-        const uint32_t line = dst + row * 128;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          store_unit(line + (((2 * c + j) ^ (row & 7)) << 4), w[i][j], lo);
-      }
+      for (int j = 0; j < D / 32; ++j)
+        store_unit((at ^ (j << 4)) + i * 1024, w[i][j], D == 128 && j >= 2 ? hi : lo);
     }
   }
-  __device__ __forceinline__ void store_v(uint32_t dst, int row0, int held, int lane) const {
-    const int c = lane >> 2, t = lane & 3;
-    const int turn = t >> 1;
+  __device__ __forceinline__ void store_v(uint32_t at, int held, int lane) const {
+    const int t = lane & 3;
+    const bool turn = t >= 2;
+    uint32_t bytes = s[0];
+    const int n = held - 4 * t;  // of this lane's four tokens
+    if (n < 4) bytes = n <= 0 ? 0u : bytes & (0xffffffffu >> (32 - 8 * n));
+    if (D == 64 && turn) {       // pieces in the other order
+      at = (at ^ 32) + 256;
+      bytes = bytes << 16 | bytes >> 16;
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int token = 4 * t + 2 * i;
-      uint32_t two = s[i];
-      if (token + 1 >= held) two = token >= held ? 0u : two & 0xffu;
-      const __half2 sc = e4m3x2_to_half2(two);
-      const __half2 s0 = __low2half2(sc), s1 = __high2half2(sc);
-      if constexpr (D == 128) {  // dims 16 c ..: panel c / 4, units 2 (c % 4), + 1
+      const __half2 two = e4m3x2_to_half2(i ? bytes >> 16 : bytes & 0xffffu);
+      const __half2 scale[2] = {__low2half2(two), __high2half2(two)};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = j >> 1, row = row0 + token + k;   // token of the pair
-          const int h = (j & 1) ^ turn;
-          const uint32_t word = turn ? w[i][2 * k + (~j & 1)] : w[i][j];
-          store_unit(dst + (c >> 2) * Layout<D>::kPanelBytes + row * 128 +
-                         (((2 * (c & 3) + h) ^ (row & 7)) << 4),
-                     word, k ? s1 : s0);
-        }
-      } else {  // dims 8 c ..: unit c
+      for (int k = 0; k < 2; ++k) {  // token of the pair
+        if constexpr (D == 128) {
+          const uint32_t a = w[i][2 * k], b = w[i][2 * k + 1];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int k = j ^ turn, row = row0 + token + k;
-          const uint32_t word = turn ? w[i][j ^ 1] : w[i][j];
-          store_unit(dst + row * 128 + ((c ^ (row & 7)) << 4), word, k ? s1 : s0);
+          for (int j = 0; j < 2; ++j)
+            store_unit((at ^ ((2 * i + k ^ j) << 4)) + (2 * i + k) * 128,
+                       turn == (j == 0) ? b : a, scale[k]);
+        } else {
+          const uint32_t row = i == 0 ? at : turn ? (at ^ 32) - 256 : (at ^ 32) + 256;
+          store_unit((row ^ (k << 4)) + k * 128, turn ? w[1 - i][k] : w[i][k], scale[k]);
         }
       }
     }
@@ -219,13 +241,17 @@ struct Share {
 // The tiles of a CTA's items one after the other, as the producers walk them
 struct TileCursor {
   int k = -1, t = 0, ntiles = 0;  // item of this CTA, tile in it
+  int w;                          // its place in the list
   int kvh, L, nblk;
   const int32_t* table;
   bool done = false;
-  __device__ __forceinline__ void next(const AttnParams& p, const PrefillWork& work, int num_items) {
+  // item(k): the place of this CTA's item k in the list, past its end if none
+  template <typename Item>
+  __device__ __forceinline__ void next(const AttnParams& p, const PrefillWork& work, int num_items,
+                                       Item item) {
     if (done) return;
     while (++t >= ntiles) {
-      const int w = item_index(++k);
+      w = item(++k);
       if (w >= num_items) {
         done = true;
         return;
@@ -258,8 +284,12 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint32_t sh_tmem_base;
   __shared__ int sh_abort;
+  __shared__ int sh_item[kItemRing];
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (from one lane: the compiler then keeps what follows from it, above all the
+  // MMA issuer's descriptors, in uniform registers; with the elected lane of its
+  // branches, 254 -> 234 us at the case named above)
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t base = ((uint32_t)__cvta_generic_to_shared(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = base + LY::q_off, sK = base + LY::k_off, sV = base + LY::v_off,
                  sBar = base + LY::bar_off;
@@ -282,6 +312,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       mbar_init(bar(kBarPFull + i), 4);  // one arrival per softmax warp of the half
       mbar_init(bar(kBarODone + i), 1);
     }
+    for (int i = 0; i < kItemRing; ++i) mbar_init(bar(kBarItem + i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     prefetch_tmap(&tm_q);
   }
@@ -292,25 +323,42 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh_tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh_tmem_base, 0);
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int num_items = work.count > 0 ? work.count : p.ws_items[0].x;
   int* status = p.ws_status;
+  // the place in the list of this CTA's item k.  (A slot of the ring is written
+  // again eight items later, which every role must have reached by then.)
+  auto item_at = [&](int k) {
+    int w = INT32_MAX;
+    if (wait_bar(bar(kBarItem + k % kItemRing), (k / kItemRing) & 1, abort_flag, status))
+      w = *(volatile int*)&sh_item[k % kItemRing];
+    return __shfl_sync(0xffffffffu, w, 0);
+  };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp != kWarpMma) {
+    if (warp != kWarpMma && warp != kWarpIdle) {
       // ============ producers: K and V tiles from codes; warp 8 the Q tiles too ============
-      // A phase is the K or the V of a tile.  A warp takes three (or two) of
-      // the phase's blocks, every third; the codes of the phase after are
+      // A phase is the K or the V of a tile.  A warp takes one or two of the
+      // phase's blocks, every sixth; the codes of the phase after are
       // loaded as each block of this one has been stored.
-      const int me = warp == kWarpQ ? 0 : warp - 9;   // 0, 1, 2
-      const int k0 = me, v0 = 2 - me;                 // its first block of a K / V phase
+      const int me = warp == kWarpQ ? 0 : warp - (warp < kWarpIdle ? 9 : 10);  // 0 .. 5
+      const int k0 = me, v0 = kProducers - 1 - me;  // its first block of a K / V phase
       const uint8_t* cache = (const uint8_t*)p.k_cache;
+      // warp 8, lane 0: item k of this CTA is number w of the list
+      auto publish = [&](int k, int w) {
+        sh_item[k % kItemRing] = w;
+        mbar_arrive(bar(kBarItem + k % kItemRing));
+        // the last CTA to run out of items leaves the counters at zero
+        if (w >= num_items && atomicAdd(p.ws_header + kWsDone, 1) == (int)gridDim.x - 1)
+          p.ws_header[kWsClaim] = p.ws_header[kWsDone] = 0;
+      };
+      if (warp == kWarpQ && lane == 0) publish(0, blockIdx.x);
       TileCursor cur, nxt;
-      nxt.next(p, work, num_items);
+      nxt.next(p, work, num_items, item_at);
       int ids_n = nxt.ids(p, lane);
       auto tile_of = [&](int ids, int b, int kvh) -> const uint8_t* {
         const int id = __shfl_sync(0xffffffffu, ids, b & 7);
@@ -318,9 +366,9 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
                    ? cache + ((int64_t)id * p.num_kv_heads + kvh) * Fp4Tile<D>::bytes
                    : nullptr;
       };
-      Share<D> sh[3];
+      Share<D> sh[2];
 #pragma unroll
-      for (int i = 0; i < 3; ++i) sh[i].load_k(tile_of(ids_n, k0 + 3 * i, nxt.kvh), lane);
+      for (int i = 0; i < 2; ++i) sh[i].load_k(tile_of(ids_n, k0 + kProducers * i, nxt.kvh), lane);
       uint32_t g = 0;  // global tile counter
       bool ok = true;
       int item = -1;
@@ -333,7 +381,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
           if (lane == 0) {
             if (item > 0) ok = wait_bar(bar(kBarQEmpty), (item - 1) & 1, abort_flag, status);
             if (ok) {
-              const ItemInfo it = load_item(p, work, item_index(item));
+              const ItemInfo it = load_item(p, work, cur.w);
               mbar_expect_tx(bar(kBarQFull), 2 * LY::kBytes);
               for (int h = 0; h < 2; ++h) {
                 const int head = pair_heads ? it.head0 + h : it.head0;
@@ -347,7 +395,15 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
         }
-        nxt.next(p, work, num_items);
+        // the item after this one, when two of its tiles are left; made known at
+        // the end of the first of them, when the counter has answered
+        const bool take = warp == kWarpQ && lane == 0 && cur.t == max(cur.ntiles - 2, 0);
+        int taken = 0;
+        if (take) {
+          taken = (int)gridDim.x + atomicAdd(p.ws_header + kWsClaim, 1);
+          if (cur.ntiles == 1) publish(cur.k + 1, taken);
+        }
+        nxt.next(p, work, num_items, item_at);
         ids_n = nxt.ids(p, lane);
         const int st = g % kStages;
         const int key0 = cur.t * KT;
@@ -360,30 +416,33 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
-          const uint32_t dst = (phase ? sV : sK) + st * LY::kBytes;
+          const uint32_t dst = phase ? sV + st * LY::kBytes + Share<D>::at_v(lane)
+                                     : sK + st * LY::kBytes + Share<D>::at_k(lane);
 #pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const int b = (phase ? v0 : k0) + 3 * i;
+          for (int i = 0; i < 2; ++i) {
+            const int b = (phase ? v0 : k0) + kProducers * i;
             if (b < kTileBlocks) {
               const int held = cur.L - key0 - b * kBlockSize;  // tokens of the block
               if (phase)
-                sh[i].store_v(dst, b * kBlockSize, held, lane);
+                sh[i].store_v(dst + b * 2048, held, lane);
               else
-                sh[i].store_k(dst, b * kBlockSize, held, lane);
+                sh[i].store_k(dst + b * 2048, held, lane);
             }
             // the same slot of the next phase: this tile's V, the next one's K
             if (phase)
-              sh[i].load_k(tile_of(ids_n, k0 + 3 * i, nxt.kvh), lane);
+              sh[i].load_k(tile_of(ids_n, k0 + kProducers * i, nxt.kvh), lane);
             else
-              sh[i].load_v(tile_of(ids, v0 + 3 * i, cur.kvh), lane);
+              sh[i].load_v(tile_of(ids, v0 + kProducers * i, cur.kvh), lane);
           }
           fence_proxy_async_smem();  // the stores, before the tensor core reads them
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(full));
+          if (elect_one()) mbar_arrive(bar(full));
         }
+        if (take && cur.ntiles > 1) publish(cur.k + 1, taken);
+        __syncwarp();
         ++g;
       }
-    } else {
+    } else if (warp == kWarpMma) {
       // =========================== MMA issuer ===========================
       // (as in the bf16 kernel: P.V of tile g-1 before Q K^T of tile g, per half)
       constexpr uint32_t idesc_qk = instr_desc(128, KT, 0, 0, 0);
@@ -397,7 +456,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         ok = wait_bar(bar(kBarPFull + h), gt & 1, abort_flag, status);
         if (!ok) return;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint64_t dv = dv0 + (uint64_t)(((gt % kStages) * LY::kBytes) >> 4);
           const uint32_t dst = tmem + kTmemO + 128 * h;
           const uint32_t pa = tmem + kTmemS + 128 * h;
@@ -410,7 +469,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         __syncwarp();
       };
       auto issue_qk = [&](int h, uint32_t gt) {  // S_h = Q_h K^T (tile gt)
-        if (lane == 0) {
+        if (elect_one()) {
           const uint64_t dk = dk0 + (uint64_t)(((gt % kStages) * LY::kBytes) >> 4);
           const uint64_t dq = dq0 + (uint64_t)((h * LY::kBytes) >> 4);
           const uint32_t dst = tmem + kTmemS + 128 * h;
@@ -424,7 +483,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         __syncwarp();
       };
       for (int k = 0; ok; ++k) {
-        const int w = item_index(k);
+        const int w = item_at(k);
         if (w >= num_items) break;
         const ItemInfo it = load_item(p, work, w);
         ok = wait_bar(bar(kBarQReady), k & 1, abort_flag, status);
@@ -440,7 +499,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
             if (t > 0) issue_pv(h, g - 1, g - 1 == g_first);  // P_h of the previous tile
             if (ok) issue_qk(h, g);
           }
-          if (ok && lane == 0) {
+          if (ok && elect_one()) {
             umma_commit(bar(kBarKEmpty + g % kStages));
             if (t > 0) umma_commit(bar(kBarVEmpty + (g - 1) % kStages));
             if (t == it.ntiles - 1) umma_commit(bar(kBarQEmpty));
@@ -452,7 +511,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
           ok = wait_bar(bar(kBarVFull + gl % kStages), (gl / kStages) & 1, abort_flag, status);
           if (ok) tc_fence_after();
           for (int h = 0; h < 2 && ok; ++h) issue_pv(h, gl, gl == g_first);
-          if (ok && lane == 0) umma_commit(bar(kBarVEmpty + gl % kStages));
+          if (ok && elect_one()) umma_commit(bar(kBarVEmpty + gl % kStages));
           __syncwarp();
         }
       }
@@ -503,11 +562,11 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarQReady));
+      if (elect_one()) mbar_arrive(bar(kBarQReady));
     };
-    if (item_index(0) < num_items) convert_q(0);
+    if (item_at(0) < num_items) convert_q(0);
     for (int k = 0; ok; ++k) {
-      const int w = item_index(k);
+      const int w = item_at(k);
       if (w >= num_items) break;
       const ItemInfo it = load_item(p, work, w);
       const int head = pair_heads ? it.head0 + h : it.head0;
@@ -611,10 +670,10 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPFull + h));
+        if (elect_one()) mbar_arrive(bar(kBarPFull + h));
       }
       // the next item's Q while this one's last P.V runs
-      if (ok && item_index(k + 1) < num_items) convert_q(k + 1);
+      if (ok && item_at(k + 1) < num_items) convert_q(k + 1);
       if (!ok || it.ntiles == 0) continue;
       // ---- epilogue: O / l to global memory
       ok = wait_bar(bar(kBarODone + h), (g - 1) & 1, abort_flag, status);
