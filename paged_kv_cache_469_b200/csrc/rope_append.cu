@@ -32,7 +32,10 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 8;
+// Small CTAs: a warp is done after two round trips to memory, and its place is
+// free at once (8 warps: 46.8 us for 8192 tokens of 32 + 2 x 8 heads of 128 in
+// bf16, 205 MB; 4 warps: 41.7)
+constexpr int kWarps = 4;
 
 // eight consecutive elements
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
@@ -121,12 +124,8 @@ rope_append_kernel(const RopeAppendParams p, int chunks, int64_t items) {
   // and lets the work after it be launched: see the other kernels
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (item >= items) return;
   const int lane = threadIdx.x & 31;
   const int l = lane % kLanes, sub = lane / kLanes;
-  const int64_t tok = item / chunks;
-  const int row0 = (int)(item % chunks) * (kRows * U) + sub;
   const int nk = p.num_q_heads, nv = nk + p.num_kv_heads, n = nv + p.num_kv_heads;
 
   // this lane's two vectors of a row: the two sides of its rotation pairs; of
@@ -142,6 +141,16 @@ rope_append_kernel(const RopeAppendParams p, int chunks, int64_t items) {
     vb = va + (rotated ? half_pairs : kLanes - half_pairs);
   }
 
+  // An item is U row sets of one token.  Its slot and position are read one
+  // item ahead, so that its rows and angles are one round trip away.
+  const int64_t step = (int64_t)gridDim.x * kWarps;
+  int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (item >= items) return;
+  int64_t tok = item / chunks, slot = p.slot_mapping[tok];
+  int64_t pos = p.rotary_dim > 0 ? p.positions[tok] : 0;
+#pragma unroll 1
+  while (true) {
+  const int row0 = (int)(item - tok * chunks) * (kRows * U) + sub;
   Raw8<T> a[U], b[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -152,26 +161,30 @@ rope_append_kernel(const RopeAppendParams p, int chunks, int64_t items) {
     a[u].load(src + 8 * va);
     b[u].load(src + 8 * vb);
   }
-  const int64_t slot = p.slot_mapping[tok];
   const bool stored = slot >= 0 && slot < (int64_t)p.num_blocks * kBlockSize;
   const int64_t blk = slot / kBlockSize;
   const int off = (int)(slot % kBlockSize);
+  // without an angle the token is left out
+  const bool placed = p.rotary_dim == 0 || (pos >= 0 && pos < p.max_position);
   float c[8], s[8];
-  if (p.rotary_dim > 0) {
-    const int64_t pos = p.positions[tok];
-    if (pos < 0 || pos >= p.max_position) return;  // no angle: the token is left out
-    if (rotated && row0 < nv) {
-      const float* t = p.cos_sin + pos * p.rotary_dim + 8 * l;
-      load8(t, c);
-      load8(t + p.rotary_dim / 2, s);
-    }
+  if (placed && rotated && row0 < nv) {
+    const float* t = p.cos_sin + pos * p.rotary_dim + 8 * l;
+    load8(t, c);
+    load8(t + p.rotary_dim / 2, s);
+  }
+  // the next item's
+  const int64_t item2 = item + step, tok1 = tok;
+  if (item2 < items) {
+    tok = item2 / chunks;
+    slot = p.slot_mapping[tok];
+    pos = p.rotary_dim > 0 ? p.positions[tok] : 0;
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int r = row0 + u * kRows;
     // every lane of the warp stays in the loop: the 4-bit groups' maxima are
     // exchanged between lanes of a row
-    const bool live = r < n && (r < nk || stored);
+    const bool live = placed && r < n && (r < nk || stored);
     float x[8], y[8];
     a[u].values(x);
     b[u].values(y);
@@ -201,6 +214,7 @@ rope_append_kernel(const RopeAppendParams p, int chunks, int64_t items) {
       const float g = is_v ? p.v_scale : p.k_scale, six_g = is_v ? p.v_six : p.k_six;
       // interleaved: a lane holds a whole group; else each half of a group
       // lies with the neighbouring lane
+      if (row0 - sub + u * kRows + kRows > nk) {  // (of the warp's rows, not this lane's)
       float ma = absmax8(x), mb = absmax8(y);
       const float oa = __shfl_xor_sync(0xffffffffu, ma, 1);
       const float ob = __shfl_xor_sync(0xffffffffu, mb, 1);
@@ -227,11 +241,12 @@ rope_append_kernel(const RopeAppendParams p, int chunks, int64_t items) {
         }
         continue;
       }
+      }
     }
     if (!live) continue;
     T* dst;
     if (r < nk) {
-      dst = (T*)p.q_out + (tok * nk + r) * (int64_t)D;
+      dst = (T*)p.q_out + (tok1 * nk + r) * (int64_t)D;
     } else {
       const int h = r - (r < nv ? nk : nv);
       dst = (T*)(r < nv ? p.k_cache : p.v_cache) +
@@ -244,6 +259,9 @@ rope_append_kernel(const RopeAppendParams p, int chunks, int64_t items) {
       a[u].store(dst + 8 * va);
       b[u].store(dst + 8 * vb);
     }
+  }
+  if (item2 >= items) break;
+  item = item2;
   }
 }
 
@@ -289,6 +307,21 @@ gather_fp4_kernel(const GatherFp4Params p, int64_t threads) {
   }
 }
 
+// CTAs of a kernel that one SM holds, asked for once per kernel and device
+template <typename Kernel>
+int resident_ctas(Kernel kernel, int threads, std::atomic<int> (&known)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess ||
+        n < 1)
+      return 1;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 cudaLaunchConfig_t dependent_launch(int64_t grid, int threads, cudaStream_t stream,
                                     cudaLaunchAttribute* attr) {
   attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -305,19 +338,27 @@ cudaLaunchConfig_t dependent_launch(int64_t grid, int threads, cudaStream_t stre
 template <typename T, int D, bool kFp4>
 cudaError_t launch_rope(const RopeAppendParams& p, cudaStream_t stream) {
   constexpr int kRows = 32 / (D / 16);
-  constexpr int kWide = 4;
+  // row sets per warp once every SM has its fill of warps: more loads in
+  // flight against more registers (8192 bf16 tokens as above: 43.1 us with two,
+  // 41.7 with three or four; quantising, 4099 tokens: 27.8, 33.1, 33.8)
+  constexpr int kWide = kFp4 ? 2 : 3;
+  static std::atomic<int> known1[64], known[64];
   const int n = p.num_q_heads + 2 * p.num_kv_heads;
   cudaLaunchAttribute attr;
-  auto go = [&](auto kernel, int u) {
+  auto go = [&](auto kernel, int u, std::atomic<int> (&known)[64]) {
     const int chunks = (n + kRows * u - 1) / (kRows * u);
     const int64_t items = (int64_t)p.num_tokens * chunks;
-    cudaLaunchConfig_t cfg =
-        dependent_launch((items + kWarps - 1) / kWarps, kWarps * 32, stream, &attr);
+    // one wave of CTAs exactly (8192 bf16 tokens as above: 37.7 us; with one
+    // more per SM than fits 48.0, one less 41.4)
+    const int64_t grid =
+        min((items + kWarps - 1) / kWarps,
+            (int64_t)device_sm_count() * resident_ctas(kernel, kWarps * 32, known));
+    cudaLaunchConfig_t cfg = dependent_launch(grid, kWarps * 32, stream, &attr);
     return cudaLaunchKernelEx(&cfg, kernel, p, chunks, items);
   };
   if ((int64_t)p.num_tokens * n <= (int64_t)device_sm_count() * 64 * kRows)
-    return go(rope_append_kernel<T, D, kFp4, 1>, 1);
-  return go(rope_append_kernel<T, D, kFp4, kWide>, kWide);
+    return go(rope_append_kernel<T, D, kFp4, 1>, 1, known1);
+  return go(rope_append_kernel<T, D, kFp4, kWide>, kWide, known);
 }
 
 }  // namespace
