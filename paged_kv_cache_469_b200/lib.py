@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 
+import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -262,18 +263,33 @@ def plan_step(free_queue: torch.Tensor, planner_state: torch.Tensor,
         raise PAError(rc, "pa_plan_step")
 
 
-def _on_device(name, fn, stream, tensors, *args):
-    """Call fn(*args, stream) with the tensors' device current.  ``tensors``: every
-    tensor of the call, by name; all must be CUDA tensors of one device."""
-    dev = tensors[0][1].get_device()
-    for what, t in tensors:
-        if t.get_device() != dev or dev < 0:
-            raise ValueError(f"{name}: {what} must be a CUDA tensor on the device of "
-                             f"{tensors[0][0]}")
-    if dev == torch.cuda.current_device():
-        s = stream.cuda_stream if stream is not None else \
-            torch._C._cuda_getCurrentRawStream(dev)
-        rc = fn(*args, s)
+FP4_BLOCK_SIZE = 16  # tokens of a block, and so of a 4-bit tile
+
+
+# The calls below are often bound by the host (a decode step's kernels take a few
+# microseconds): their checks are plain expressions, and name the offender only
+# once one has failed.
+
+def _refuse_devices(**tensors) -> None:
+    first, dev = next((n, t.get_device()) for n, t in tensors.items())
+    for name, t in tensors.items():
+        if t.get_device() < 0 or t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor, on the device of {first}")
+
+
+def _refuse_strided(**tensors) -> None:
+    for name, t in tensors.items():
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _call(name, dev: int, stream, *args) -> None:
+    """The C call ``name`` on ``stream`` (None: the current one of device ``dev``), with
+    that device current."""
+    fn = getattr(library(), name)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, _stream(stream))
@@ -281,31 +297,40 @@ def _on_device(name, fn, stream, tensors, *args):
         raise PAError(rc, name)
 
 
-def _contiguous(*named) -> None:
-    for what, t in named:
-        if not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous")
-
-
 def _rows(t: torch.Tensor, name: str, tokens: int, heads: int, d: int) -> int:
     """Elements from one token's row to the next of a [tokens][heads][d] tensor
     whose rows are contiguous (a slice of a fused projection, for instance)."""
-    st = t.stride()
-    if t.shape != (tokens, heads, d) or (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
+    row, head, one = t.stride()
+    if (head != d and heads > 1) or (one != 1 and d > 1):
         raise ValueError(f"{name} must be [{tokens}, {heads}, {d}] with contiguous rows")
-    return st[0] if tokens > 1 else heads * d
+    return row if tokens > 1 else heads * d
 
 
-def _rope_arguments(q, k, v, d, slot_mapping, positions, cos_sin, q_out):
-    """The arguments that both appends pass on alike, after their checks."""
-    t, hkv = k.shape[0], k.shape[1]
-    hq = q.shape[1]
-    if q.dtype != k.dtype or v.dtype != k.dtype or q_out.dtype != k.dtype:
+def _append(name, q, k, v, caches, scales, slot_mapping, positions, cos_sin, q_out, interleaved,
+            hkv, d, num_blocks, stream) -> torch.Tensor:
+    """Both appends: the checks they share, and the call."""
+    t, hq, _ = q.shape
+    if q_out is None:
+        q_out = torch.empty(t, hq, d, dtype=q.dtype, device=q.device)
+    dt = k.dtype
+    if q.dtype != dt or v.dtype != dt or q_out.dtype != dt:
         raise TypeError("q, k, v and q_out must have one dtype")
     if slot_mapping.dtype != torch.int64:
         raise TypeError("slot_mapping must be int64")
-    if q_out.shape != (t, hq, d) or slot_mapping.shape != (t,):
-        raise ValueError("inconsistent sizes of q_out or slot_mapping")
+    rows = (t, hkv, d)
+    if k.shape != rows or v.shape != rows or q.shape != (t, hq, d) or q_out.shape != q.shape or \
+            slot_mapping.shape != (t,):
+        raise ValueError("the sizes of q, k, v, q_out, slot_mapping and the cache do not fit")
+    dev = k.get_device()
+    if dev < 0 or q.get_device() != dev or v.get_device() != dev or \
+            q_out.get_device() != dev or slot_mapping.get_device() != dev or \
+            caches[0].get_device() != dev or caches[-1].get_device() != dev:
+        _refuse_devices(k=k, q=q, v=v, q_out=q_out, slot_mapping=slot_mapping, cache=caches[0],
+                        v_cache=caches[-1])
+    if not (q_out.is_contiguous() and slot_mapping.is_contiguous() and
+            caches[0].is_contiguous() and caches[-1].is_contiguous()):
+        _refuse_strided(q_out=q_out, slot_mapping=slot_mapping, cache=caches[0],
+                        v_cache=caches[-1])
     rotary, longest, pos_ptr, cs_ptr = 0, 0, None, None
     if cos_sin is not None:
         if positions is None or positions.dtype != torch.int64:
@@ -314,17 +339,18 @@ def _rope_arguments(q, k, v, d, slot_mapping, positions, cos_sin, q_out):
             raise TypeError("cos_sin must be a float32 [max_position, rotary_dim] tensor")
         if positions.shape != (t,):
             raise ValueError("inconsistent size of positions")
-        _contiguous(("positions", positions), ("cos_sin", cos_sin))
+        if positions.get_device() != dev or cos_sin.get_device() != dev:
+            _refuse_devices(k=k, positions=positions, cos_sin=cos_sin)
+        if not (positions.is_contiguous() and cos_sin.is_contiguous()):
+            _refuse_strided(positions=positions, cos_sin=cos_sin)
         longest, rotary = cos_sin.shape
         pos_ptr, cs_ptr = positions.data_ptr(), cos_sin.data_ptr()
-    _contiguous(("q_out", q_out), ("slot_mapping", slot_mapping))
-    head = (q_out.data_ptr(), q.data_ptr(), _rows(q, "q", t, hq, d), k.data_ptr(),
-            _rows(k, "k", t, hkv, d), v.data_ptr(), _rows(v, "v", t, hkv, d))
-    tail = (slot_mapping.data_ptr(), pos_ptr, cs_ptr, longest, rotary)
-    tensors = [("k", k), ("q", q), ("v", v), ("q_out", q_out), ("slot_mapping", slot_mapping)]
-    if cos_sin is not None:
-        tensors += [("positions", positions), ("cos_sin", cos_sin)]
-    return head, tail, tensors, t, hq, hkv
+    _call(name, dev, stream, q_out.data_ptr(), q.data_ptr(), _rows(q, "q", t, hq, d),
+          k.data_ptr(), _rows(k, "k", t, hkv, d), v.data_ptr(), _rows(v, "v", t, hkv, d),
+          *[c.data_ptr() for c in caches], *scales, slot_mapping.data_ptr(), pos_ptr, cs_ptr,
+          longest, rotary, int(interleaved), t, hq, hkv, d, FP4_BLOCK_SIZE, num_blocks,
+          _dtype_code(k))
+    return q_out
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -341,23 +367,13 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torc
     cosines and then the sines of a position's angles (None: nothing is
     rotated).  Returns q_out (a new tensor unless given)."""
     num_blocks, hkv, bs, d = k_cache.shape
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    head, tail, tensors, t, hq, heads = _rope_arguments(q, k, v, d, slot_mapping, positions,
-                                                        cos_sin, q_out)
-    if heads != hkv or v_cache.shape != k_cache.shape:
-        raise ValueError("rope_append: the caches' shapes do not fit k and v")
+    if bs != FP4_BLOCK_SIZE or v_cache.shape != k_cache.shape:
+        raise ValueError("rope_append: the caches' shapes do not fit")
     if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
         raise TypeError("the caches must have the dtype of k")
-    _contiguous(("k_cache", k_cache), ("v_cache", v_cache))
-    _on_device("pa_rope_append", library().pa_rope_append, stream,
-               tensors + [("k_cache", k_cache), ("v_cache", v_cache)], *head,
-               k_cache.data_ptr(), v_cache.data_ptr(), *tail, int(interleaved), t, hq, hkv, d,
-               bs, num_blocks, _dtype_code(k))
-    return q_out
-
-
-FP4_BLOCK_SIZE = 16  # tokens of a block, and so of a tile
+    return _append("pa_rope_append", q, k, v, (k_cache, v_cache), (),
+                   slot_mapping, positions, cos_sin, q_out, interleaved, hkv, d, num_blocks,
+                   stream)
 
 
 def new_fp4_cache(num_blocks: int, num_kv_heads: int, head_dim: int,
@@ -371,7 +387,6 @@ def _fp4_cache(kv_cache: torch.Tensor):
     num_blocks, hkv, tile = kv_cache.shape
     if kv_cache.dtype != torch.uint8 or tile % 18:
         raise TypeError("kv_cache must be uint8 [num_blocks, num_kv_heads, 18 * head_dim]")
-    _contiguous(("kv_cache", kv_cache))
     return num_blocks, hkv, tile // 18
 
 
@@ -383,17 +398,9 @@ def rope_append_fp4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_cache:
     """``rope_append`` into a 4-bit cache (see pa_rope_append_fp4 in pa.h); k_scale and
     v_scale are the tensors' own scales."""
     num_blocks, hkv, d = _fp4_cache(kv_cache)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    head, tail, tensors, t, hq, heads = _rope_arguments(q, k, v, d, slot_mapping, positions,
-                                                        cos_sin, q_out)
-    if heads != hkv:
-        raise ValueError("rope_append_fp4: the cache's shape does not fit k and v")
-    _on_device("pa_rope_append_fp4", library().pa_rope_append_fp4, stream,
-               tensors + [("kv_cache", kv_cache)], *head, kv_cache.data_ptr(), float(k_scale),
-               float(v_scale), *tail, int(interleaved), t, hq, hkv, d, FP4_BLOCK_SIZE,
-               num_blocks, _dtype_code(k))
-    return q_out
+    return _append("pa_rope_append_fp4", q, k, v, (kv_cache,),
+                   (float(k_scale), float(v_scale)), slot_mapping, positions, cos_sin, q_out,
+                   interleaved, hkv, d, num_blocks, stream)
 
 
 def gather_fp4(kv_cache: torch.Tensor, slots: torch.Tensor, *, k_scale: float = 1.0,
@@ -413,12 +420,15 @@ def gather_fp4(kv_cache: torch.Tensor, slots: torch.Tensor, *, k_scale: float = 
         raise ValueError("gather_fp4: k_out and v_out must be [n, num_kv_heads, head_dim]")
     if v_out.dtype != k_out.dtype:
         raise TypeError("k_out and v_out must have one dtype")
-    _contiguous(("slots", slots), ("k_out", k_out), ("v_out", v_out))
-    _on_device("pa_gather_fp4", library().pa_gather_fp4, stream,
-               [("kv_cache", kv_cache), ("slots", slots), ("k_out", k_out), ("v_out", v_out)],
-               k_out.data_ptr(), v_out.data_ptr(), kv_cache.data_ptr(), float(k_scale),
-               float(v_scale), slots.data_ptr(), n, hkv, d, FP4_BLOCK_SIZE, num_blocks,
-               _dtype_code(k_out))
+    dev = kv_cache.get_device()
+    if dev < 0 or not (slots.get_device() == k_out.get_device() == v_out.get_device() == dev):
+        _refuse_devices(kv_cache=kv_cache, slots=slots, k_out=k_out, v_out=v_out)
+    if not (kv_cache.is_contiguous() and slots.is_contiguous() and k_out.is_contiguous() and
+            v_out.is_contiguous()):
+        _refuse_strided(kv_cache=kv_cache, slots=slots, k_out=k_out, v_out=v_out)
+    _call("pa_gather_fp4", dev, stream, k_out.data_ptr(), v_out.data_ptr(), kv_cache.data_ptr(),
+          float(k_scale), float(v_scale), slots.data_ptr(), n, hkv, d, FP4_BLOCK_SIZE, num_blocks,
+          _dtype_code(k_out))
     return k_out, v_out
 
 
@@ -430,9 +440,23 @@ def new_fp4_workspace(num_seqs: int, num_tokens: int, num_q_heads: int, num_kv_h
     if n == 0:
         raise ValueError("invalid workspace bounds")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
-    _on_device("pa_workspace_init", library().pa_workspace_init, stream, [("workspace", ws)],
-               ws.data_ptr(), n)
+    if not ws.is_cuda:
+        raise ValueError("the workspace must be on a CUDA device")
+    _call("pa_workspace_init", ws.get_device(), stream, ws.data_ptr(), n)
     return ws
+
+
+def _host_lengths(a, n: int):
+    """(pointer, keep-alive) of n host lengths, or (None, None)."""
+    if a is None:
+        return None, None
+    if isinstance(a, torch.Tensor):
+        a = a.cpu().numpy()
+    if not (isinstance(a, np.ndarray) and a.dtype == np.int32 and a.flags.c_contiguous):
+        a = np.ascontiguousarray(a, dtype=np.int32)
+    if a.shape != (n,):
+        raise ValueError("a host copy's size does not fit")
+    return a.__array_interface__["data"][0], a
 
 
 def attention_varlen_fp4(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor,
@@ -454,21 +478,24 @@ def attention_varlen_fp4(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Ten
     if qd != d or out.shape != q.shape or block_tables.shape[0] != s or \
             query_start_loc.shape[0] != s + 1:
         raise ValueError("attention_varlen_fp4: inconsistent sizes")
-    _contiguous(("out", out), ("q", q), ("block_tables", block_tables), ("seq_lens", seq_lens),
-                ("query_start_loc", query_start_loc), ("workspace", workspace))
-    sl_ptr, sl_keep = _host_i32(seq_lens_host)
-    qs_ptr, qs_keep = _host_i32(query_start_loc_host)
-    if (sl_ptr and sl_keep.shape != (s,)) or (qs_ptr and qs_keep.shape != (s + 1,)):
-        raise ValueError("attention_varlen_fp4: the host copies' sizes do not fit")
-    _on_device("pa_attention_varlen_fp4", library().pa_attention_varlen_fp4, stream,
-               [("q", q), ("out", out), ("kv_cache", kv_cache), ("block_tables", block_tables),
-                ("seq_lens", seq_lens), ("query_start_loc", query_start_loc),
-                ("workspace", workspace)],
-               out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), float(k_scale),
-               float(v_scale), block_tables.data_ptr(), block_tables.shape[1],
-               seq_lens.data_ptr(), query_start_loc.data_ptr(), s, t, max_query_len,
-               max_seq_len, hq, hkv, d, FP4_BLOCK_SIZE, num_blocks, float(scale),
-               _dtype_code(q), workspace.data_ptr(),
-               workspace.numel() * workspace.element_size(), sl_ptr, qs_ptr)
+    dev = q.get_device()
+    if dev < 0 or not (out.get_device() == kv_cache.get_device() == block_tables.get_device() ==
+                       seq_lens.get_device() == query_start_loc.get_device() ==
+                       workspace.get_device() == dev):
+        _refuse_devices(q=q, out=out, kv_cache=kv_cache, block_tables=block_tables,
+                        seq_lens=seq_lens, query_start_loc=query_start_loc, workspace=workspace)
+    if not (out.is_contiguous() and q.is_contiguous() and kv_cache.is_contiguous() and
+            block_tables.is_contiguous() and seq_lens.is_contiguous() and
+            query_start_loc.is_contiguous() and workspace.is_contiguous()):
+        _refuse_strided(q=q, out=out, kv_cache=kv_cache, block_tables=block_tables,
+                        seq_lens=seq_lens, query_start_loc=query_start_loc, workspace=workspace)
+    sl_ptr, sl_keep = _host_lengths(seq_lens_host, s)
+    qs_ptr, qs_keep = _host_lengths(query_start_loc_host, s + 1)
+    _call("pa_attention_varlen_fp4", dev, stream, out.data_ptr(), q.data_ptr(),
+          kv_cache.data_ptr(), float(k_scale), float(v_scale), block_tables.data_ptr(),
+          block_tables.shape[1], seq_lens.data_ptr(), query_start_loc.data_ptr(), s, t,
+          max_query_len, max_seq_len, hq, hkv, d, FP4_BLOCK_SIZE, num_blocks, float(scale),
+          _dtype_code(q), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          sl_ptr, qs_ptr)
     del sl_keep, qs_keep
     return out
