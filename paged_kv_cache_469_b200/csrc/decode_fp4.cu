@@ -107,6 +107,15 @@ struct PartMeta {
 struct Seq {
   int q0, ql, L, nblk, rgs;
 };
+// The parts of one unit that this CTA joins
+struct Run {
+  int w0;               // the warp whose last part starts the unit (or, of a unit that
+                        // starts in an earlier CTA, whose first part is the first here)
+  unsigned mine;        // the warps whose first parts belong to it
+  int before, complete; // starts in an earlier CTA; starts and ends here
+  int q0, head, row0, nrows;
+};
+
 template <typename S>
 struct Shared {
   unsigned long long bars[S::kWarps * S::kStages];
@@ -115,6 +124,9 @@ struct Shared {
   // of the sequences under way: q0, ql, L (as read), and their blocks on the
   // line summed over the warp that read them
   int4 seqs[S::kWarps * 32];
+  Run runs[S::kWarps + 1];
+  int nruns;
+  int cut[2];  // this CTA's stretch
   int abort;
   int last[2];
 };
@@ -131,15 +143,19 @@ __device__ __forceinline__ Seq load_seq(const Fp4AttnParams& p, int s) {
   return make_seq<R>(p, q0, p.query_start_loc[s + 1] - q0, p.seq_lens[s]);
 }
 
-// a / b for 0 <= a, 0 < b: from the quotient in fp32, off by one at most below
-// 2^22, where its error is under 2^22 * 2^-22
+// a / b for 0 <= a, 0 < b, in a dozen instructions: code that a launch runs once
+// costs what its fetch costs.  The first quotient is off by at most 2^31 * 2^-22,
+// the second by one.
 __device__ __forceinline__ int divide(int a, int b) {
-  if (a >= 1 << 22) return a / b;
-  int q = (int)__fdividef((float)a, (float)b);
+  const float inv = __fdividef(1.f, (float)b);
+  int q = (int)((float)a * inv);
+  q += (int)((float)(a - q * b) * inv);
   const int r = a - q * b;
-  if (r < 0) --q;
-  if (r >= b) ++q;
-  return q;
+  return q + (r >= b) - (r < 0);
+}
+// query token of a row of a kv-head: row / group
+__device__ __forceinline__ int token_of(const Fp4AttnParams& p, int row) {
+  return p.group_inv ? (int)__umulhi((unsigned)row, p.group_inv) : row;
 }
 
 // A position on the line, walked block by block over units and sequences.
@@ -271,16 +287,17 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
         return w * 32 + i;
       };
       const int end = __shfl_sync(0xffffffffu, upto, W - 1);
-      if (step == 1) {
+      if (step == 1) {  // by the thread whose sequence holds the cut
+        const int4 q = sh.seqs[threadIdx.x];
+        const int mine = q.w + (warp == 0 ? base : __shfl_sync(0xffffffffu, upto, max(warp - 1, 0)));
+        const Seq sq = make_seq<R>(p, q.x, q.y, q.z);
+        const int start = mine - sq.nblk * sq.rgs * p.num_kv_heads;
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
-          int at = min((long long)(blockIdx.x + i) * per, (long long)INT32_MAX);
-          if (at < base || at >= end) continue;
-          int pre;
-          const int nblk = (sh.seqs[find(at, &pre)].z + kBlockSize - 1) / kBlockSize;
-          const int r = at - pre - divide(at - pre, nblk) * nblk;
-          if (nblk <= S::kWhole) at += 2 * r < nblk ? -r : nblk - r;
-          (i == 0 ? cta0 : cta1) = at;
+          const int at = min((long long)(blockIdx.x + i) * per, (long long)INT32_MAX);
+          if (at < start || at >= mine) continue;
+          const int r = at - start - divide(at - start, sq.nblk) * sq.nblk;
+          sh.cut[i] = sq.nblk > S::kWhole ? at : at + (2 * r < sq.nblk ? -r : sq.nblk - r);
         }
       }
       if (step == 2) {
@@ -298,9 +315,15 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
       // at least a block per warp: fewer CTAs take a short line
       per = max(divide(base + (int)gridDim.x - 1, (int)gridDim.x), W);
       if ((long long)blockIdx.x * per >= base) return;
-      cta0 = cta1 = base;
+      if (threadIdx.x < 2) sh.cut[threadIdx.x] = base;
+      __syncthreads();
     }
-    if (step == 1 && cta0 >= cta1) return;
+    if (step == 1) {
+      __syncthreads();
+      cta0 = sh.cut[0];
+      cta1 = sh.cut[1];
+      if (cta0 >= cta1) return;
+    }
   }
 
   const int pos0 = warp_start(warp), pos1 = warp_start(warp + 1);
@@ -378,7 +401,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int row = n * 8 + g;
-        const int rr = cu.rg * R + row, j = divide(rr, p.group);
+        const int rr = cu.rg * R + row, j = token_of(p, rr);
         const T* src = (const T*)p.q +
                        ((int64_t)(cu.q.q0 + j) * p.num_q_heads + cu.head * p.group +
                         (rr - j * p.group)) * D +
@@ -416,13 +439,12 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
         for (int i = 0; i < S::kChunkK; ++i) mx = fmaxf(mx, fabsf(x[i]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // the exponent of the row's largest value (-127 for subnormals and
-        // zeros; infinities and NaN stay what they are).  Two factors: 2^127
-        // and 2^-128 alone are no normal fp32 numbers
-        const int e = (__float_as_int(mx) >> 23) - 127, e1 = e / 2;
-        const float f1 = exp2i(-e1), f2 = exp2i(e1 - e);
+        // the exponent of the row's largest value, as far as 2^-e is a normal
+        // number (beyond: nearly so; infinities and NaN stay what they are)
+        const int e = min(max((__float_as_int(mx) >> 23) - 127, -126), 126);
+        const float f = exp2i(-e);
 #pragma unroll
-        for (int i = 0; i < S::kChunkK; ++i) x[i] = x[i] * f1 * f2;
+        for (int i = 0; i < S::kChunkK; ++i) x[i] *= f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
@@ -438,9 +460,9 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int er = __shfl_sync(0xffffffffu, e, (2 * t + c) * 4);
-          sl2[n][c] = p.scale_log2 * exp2i(er / 2) * exp2i(er - er / 2);
+          sl2[n][c] = p.scale_log2 * exp2i(er);
           const int r2 = cu.rg * R + n * 8 + 2 * t + c;
-          lim[n][c] = n * 8 + 2 * t + c < nrows ? cu.q.L - cu.q.ql + divide(r2, p.group) : cu.q.L - 1;
+          lim[n][c] = n * 8 + 2 * t + c < nrows ? cu.q.L - cu.q.ql + token_of(p, r2) : cu.q.L - 1;
         }
       }
 
@@ -656,7 +678,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
             y[2 * i + 1] = o[n][i][c + 2] * f;
           }
           if (whole) {
-            const int rr = cu.rg * R + row, j = divide(rr, p.group);
+            const int rr = cu.rg * R + row, j = token_of(p, rr);
             store_row((T*)p.out +
                           ((int64_t)(cu.q.q0 + j) * p.num_q_heads + cu.head * p.group +
                            (rr - j * p.group)) * D +
@@ -690,102 +712,96 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
   __syncthreads();
   if (sh.abort) return;
 
-  // ---- join the parts.  A run: the parts of one unit in this CTA, in order:
-  // the last part of the warp where it starts (or the first part of warp 0, of
-  // a unit that starts in an earlier CTA) and the first parts that follow
-  unsigned starts, firsts, ends;
-  {
-    const bool in = lane < W;
-    const bool v0 = in && sh.meta[lane][0].valid, v1 = in && sh.meta[lane][1].valid;
-    firsts = __ballot_sync(0xffffffffu, v0);
-    ends = __ballot_sync(0xffffffffu, v0 && sh.meta[lane][0].ended);
-    starts = __ballot_sync(0xffffffffu, v1);
+  // ---- join the parts: runs of parts of one unit, in order
+  if (warp == 0) {
+    const bool v0 = lane < W && sh.meta[lane % W][0].valid;
+    const bool v1 = lane < W && sh.meta[lane % W][1].valid;
+    const unsigned firsts = __ballot_sync(0xffffffffu, v0);
+    const unsigned starts = __ballot_sync(0xffffffffu, v1);
+    const unsigned ends = __ballot_sync(0xffffffffu, v0 && sh.meta[lane % W][0].ended);
+    // a unit from an earlier CTA: the first warp with a first part, if no unit
+    // starts in a warp before it
+    const int lead = firsts ? __ffs(firsts) - 1 : 31;
+    const bool carried = firsts && (starts & ((1u << lead) - 1)) == 0;
+    auto put = [&](bool before) {
+      unsigned mine = firsts & (~0u << (lane + (before ? 0 : 1)));
+      const unsigned end = ends & mine;
+      if (end) mine &= (end & -end) | ((end & -end) - 1);
+      const PartMeta& pm = sh.meta[lane][before ? 0 : 1];
+      sh.runs[before ? 0 : __popc(starts & ((1u << lane) - 1)) + carried] =
+          Run{lane, mine, before, end && !before, pm.q0, pm.head, pm.row0, pm.nrows};
+    };
+    if (v1) put(false);
+    if (carried && lane == lead) put(true);
+    if (lane == 0) sh.nruns = __popc(starts) + carried;
   }
-  // a unit from an earlier CTA: its run starts at the first warp with a first
-  // part before any unit starts here
-  const int lead = firsts ? __ffs(firsts) - 1 : 32;
-  const bool carried = lead < 32 && (starts & ((1u << lead) - 1)) == 0;
-  const int nruns = __popc(starts) + (carried ? 1 : 0);
-  unsigned rest = starts;
-  bool pending[2] = {false, false};   // a part of a unit that other CTAs hold too
-  PartMeta far[2];
-  for (int r = 0; r < nruns; ++r) {
-    const bool from_before = carried && r == 0;
-    int w0;
-    if (from_before) {
-      w0 = lead;
+  __syncthreads();
+  const int nruns = sh.nruns;
+  // a weight per (run, row) and part, written over the part's maximum
+  for (int i = threadIdx.x; i < nruns * R; i += W * 32) {
+    const Run& run = sh.runs[i / R];
+    const int row = i % R;
+    if (row >= run.nrows) continue;
+    const unsigned mine = run.mine;
+    float* start = sh.ml[run.w0][1][row];
+    float mx = -INFINITY, sum = 0.f;
+    auto for_each_part = [&](auto visit) {  // in the order of the keys
+      if (!run.before) visit(start);
+#pragma unroll 1
+      for (unsigned left = mine; left; left &= left - 1) visit(sh.ml[__ffs(left) - 1][0][row]);
+    };
+    for_each_part([&](const float* ml) { mx = fmaxf(mx, ml[0]); });
+    for_each_part([&](float* ml) {
+      const float wt = ml[0] == -INFINITY ? 0.f : ex2(ml[0] - mx);
+      sum = fmaf(wt, ml[1], sum);
+      ml[0] = wt;
+    });
+    if (run.complete) {
+      start[1] = p.v_scale / sum;  // (its own sum has been read)
     } else {
-      w0 = __ffs(rest) - 1;
-      rest &= rest - 1;
-    }
-    // the warps whose first parts belong to the run
-    unsigned mine = firsts & (from_before ? ~0u << w0 : w0 == 31 ? 0u : ~0u << (w0 + 1));
-    const unsigned end = ends & mine;
-    const bool ended = end != 0;
-    if (ended) mine &= (end & -end) | ((end & -end) - 1);
-    const PartMeta& pm = sh.meta[w0][from_before ? 0 : 1];
-    const int nrows = pm.nrows;
-    const bool complete = ended && !from_before;
-    const int side = from_before ? 0 : 1;
-    if (!complete) {
-      pending[side] = true;
-      far[side] = pm;
-    }
-    // the rows of all runs go round the warps
-    for (int row = (warp + W * R - r * R) % W; row < nrows; row += W) {
-      // weights of the parts: lane w that of warp w's first part, lane 31 that
-      // of the part the unit starts with
-      float mi = -INFINITY, li = 0.f;
-      const bool first = lane < W && (mine >> lane & 1);
-      const bool last = !from_before && lane == 31;
-      if (first || last) {
-        const float* ml = sh.ml[last ? w0 : lane][last ? 1 : 0][row];
-        mi = ml[0];
-        li = ml[1];
-      }
-      float mx = mi;
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-      const float wt = mi == -INFINITY ? 0.f : ex2(mi - mx);
-      float sum = li * wt;
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-      float y[D / 32];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) y[i] = 0.f;
-      const int off = row * D + lane * (D / 32);
-      float v[W + 1][D / 32];  // the parts, all their loads before any sum
-#pragma unroll
-      for (int w = 0; w <= W; ++w) {
-        const float* part = (const float*)(w < W ? smem + S::part_off + w * S::kPart
-                                                 : smem + S::ring_off + w0 * S::kRing) + off;
-        const bool in = w < W ? mine >> w & 1 : !from_before;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) v[w][i] = in ? part[i] : 0.f;
-      }
-#pragma unroll
-      for (int w = W; w >= 0; --w) {
-        const float f = __shfl_sync(0xffffffffu, wt, w < W ? w : 31);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) y[i] = fmaf(f, v[w][i], y[i]);
-      }
-      if (complete) {
-        const int rr = pm.row0 + row, j = divide(rr, p.group);
-        T* dst = (T*)p.out + ((int64_t)(pm.q0 + j) * p.num_q_heads + pm.head * p.group +
-                              (rr - j * p.group)) * D + lane * (D / 32);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) dst[i] = (T)(y[i] * (p.v_scale / sum));
-      } else {
-        const int64_t at = (int64_t)(blockIdx.x * 2 + side) * 16 + row;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) p.ws_o[at * D + lane * (D / 32) + i] = y[i];
-        if (lane == 0) {
-          p.ws_ml[at * 2] = mx;
-          p.ws_ml[at * 2 + 1] = sum;
-        }
-      }
+      const int64_t at = (int64_t)(blockIdx.x * 2 + !run.before) * 16 + row;
+      *(float2*)(p.ws_ml + at * 2) = make_float2(mx, sum);
     }
   }
+  __syncthreads();
+  // four dims of a row per thread
+  constexpr int kQuads = D / 4;
+  for (int i = threadIdx.x; i < nruns * R * kQuads; i += W * 32) {
+    const Run& run = sh.runs[i / (R * kQuads)];
+    const int row = i / kQuads % R, off = row * D + i % kQuads * 4;
+    if (row >= run.nrows) continue;
+    const unsigned mine = run.mine;
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](const unsigned char* part, float f) {
+      const float4 v = *(const float4*)((const float*)part + off);
+      y[0] = fmaf(f, v.x, y[0]);
+      y[1] = fmaf(f, v.y, y[1]);
+      y[2] = fmaf(f, v.z, y[2]);
+      y[3] = fmaf(f, v.w, y[3]);
+    };
+    if (!run.before) add(smem + S::ring_off + run.w0 * S::kRing, sh.ml[run.w0][1][row][0]);
+#pragma unroll 2
+    for (unsigned left = mine; left; left &= left - 1) {
+      const int w = __ffs(left) - 1;
+      add(smem + S::part_off + w * S::kPart, sh.ml[w][0][row][0]);
+    }
+    if (run.complete) {
+      const float f = sh.ml[run.w0][1][row][1];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] *= f;
+      const int rr = run.row0 + row, j = token_of(p, rr);
+      store_dims<T>((T*)p.out + ((int64_t)(run.q0 + j) * p.num_q_heads + run.head * p.group +
+                                 (rr - j * p.group)) * D + i % kQuads * 4,
+                    y);
+    } else {
+      *(float4*)(p.ws_o + ((int64_t)(blockIdx.x * 2 + !run.before) * 16 * D + off)) =
+          make_float4(y[0], y[1], y[2], y[3]);
+    }
+  }
+  // the units that other CTAs hold parts of too: one from before this CTA, one
+  // that goes on after it
+  const Run& tail = sh.runs[max(nruns - 1, 0)];
+  const bool pending[2] = {nruns > 0 && sh.runs[0].before, nruns > 0 && !tail.before && !tail.complete};
   if (!pending[0] && !pending[1]) return;
 
   // ---- a unit in several CTAs: the one that arrives last joins its parts, in
@@ -794,8 +810,8 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
   __syncthreads();
   if (threadIdx.x < 2) {
     int mine = 0;
-    if (pending[threadIdx.x]) {
-      const PartMeta& f = far[threadIdx.x];
+    if (threadIdx.x == 0 ? pending[0] : pending[1]) {
+      const PartMeta& f = threadIdx.x == 0 ? sh.meta[sh.runs[0].w0][0] : sh.meta[tail.w0][1];
       const int c0 = divide(f.unit_start, per), c1 = divide(f.unit_start + f.nblk - 1, per);
       mine = atomicAdd(p.ws_counters + c0, 1) == c1 - c0;
       if (mine) p.ws_counters[c0] = 0;  // every part has arrived: zero for the next call
@@ -807,36 +823,41 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
   for (int side = 0; side < 2; ++side) {
     if (!sh.last[side]) continue;
     __threadfence();
-    const PartMeta f = far[side];
+    const PartMeta& f = side == 0 ? sh.meta[sh.runs[0].w0][0] : sh.meta[tail.w0][1];
     const int c0 = divide(f.unit_start, per), c1 = divide(f.unit_start + f.nblk - 1, per);
     for (int row = warp; row < f.nrows; row += W) {
       auto slot = [&](int c) { return (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * 16 + row; };
-      float mx = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, __ldcg(p.ws_ml + slot(c) * 2));
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-      float y[D / 32], sum = 0.f;
+      float y[D / 32], sum = 0.f, mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) y[i] = 0.f;
       for (int cc = c0; cc <= c1; cc += 32) {  // a lane's weight each, then the parts
         const int c = cc + lane;
-        float wt = 0.f;
-        if (c <= c1) {
-          const float2 ml = __ldcg((const float2*)(p.ws_ml + slot(c) * 2));
-          wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
-          sum = fmaf(wt, ml.y, sum);
-        }
-#pragma unroll 8
-        for (int i = cc; i <= min(c1, cc + 31); ++i) {
-          const float f1 = __shfl_sync(0xffffffffu, wt, i - cc);
+        const float2 ml = c <= c1 ? __ldcg((const float2*)(p.ws_ml + slot(c) * 2))
+                                  : make_float2(-INFINITY, 0.f);
+        float top = ml.x;
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            y[k] = fmaf(f1, __ldcg(p.ws_o + slot(i) * D + lane * (D / 32) + k), y[k]);
+        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        if (top > mx) {
+          const float old = ex2(mx - top);
+          mx = top;
+          sum *= old;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) y[i] *= old;
+        }
+        const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
+        sum = fmaf(wt, ml.y, sum);
+        const int n = min(c1 - cc + 1, 32);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+          const float f1 = __shfl_sync(0xffffffffu, wt, i);
+          const float* part = p.ws_o + slot(cc + i) * D + lane * (D / 32);
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) y[k] = fmaf(f1, __ldcg(part + k), y[k]);
         }
       }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-      const int rr = f.row0 + row, j = divide(rr, p.group);
+      const int rr = f.row0 + row, j = token_of(p, rr);
       T* dst = (T*)p.out + ((int64_t)(f.q0 + j) * p.num_q_heads + f.head * p.group +
                             (rr - j * p.group)) * D + lane * (D / 32);
 #pragma unroll

@@ -243,6 +243,7 @@ extern "C" int pa_attention_varlen_fp4(
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = num_kv_heads;
   p.group = group;
+  p.group_inv = group == 1 ? 0u : (unsigned)(((1ull << 32) + group - 1) / group);
   p.num_blocks = num_blocks;
   p.scale_log2 = scale * k_scale * 1.4426950408889634f;
   p.v_scale = v_scale;

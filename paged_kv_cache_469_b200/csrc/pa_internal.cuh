@@ -196,6 +196,7 @@ struct Fp4AttnParams {
   int num_q_heads;
   int num_kv_heads;
   int group;
+  unsigned group_inv;  // ceil(2^32 / group): row / group by a high product (0: group is 1)
   int num_blocks;
   float scale_log2;  // scale * k_scale * log2(e)
   float v_scale;

@@ -528,8 +528,8 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
     uint32_t g = 0;
     bool ok = true;
     // this row of item k's Q from bf16 to f16 in place, times 2^-e (e: the
-    // exponent of its largest value; two factors, since 2^127 and 2^-128 alone
-    // are no normal fp32 numbers); sets the scale of the row's scores
+    // exponent of its largest value, as far as 2^-e is a normal number); sets the
+    // scale of the row's scores
     float sl2_next = 0.f;
     auto convert_q = [&](int k) {
       ok = wait_bar(bar(kBarQFull), k & 1, abort_flag, status);
@@ -546,15 +546,15 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
 #pragma unroll
       for (int i = 0; i < D / 2; ++i)
         top = max(top, max(q[i] & 0x7fffu, q[i] >> 16 & 0x7fffu));
-      const int e = (int)(top >> 7) - 127, e1 = e / 2;
-      const float f1 = exp2i(-e1), f2 = exp2i(e1 - e);
-      sl2_next = p.scale_log2 * exp2i(e1) * exp2i(e - e1);
+      const int e = min(max((int)(top >> 7) - 127, -126), 126);
+      const float f = exp2i(-e);
+      sl2_next = p.scale_log2 * exp2i(e);
 #pragma unroll
       for (int u = 0; u < D / 8; ++u) {
 #pragma unroll
         for (int i = 4 * u; i < 4 * u + 4; ++i)
-          q[i] = pack_f16x2(__uint_as_float(q[i] << 16) * f1 * f2,
-                            __uint_as_float(q[i] & 0xffff0000u) * f1 * f2);
+          q[i] = pack_f16x2(__uint_as_float(q[i] << 16) * f,
+                            __uint_as_float(q[i] & 0xffff0000u) * f);
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
                          line + (u / 8) * LY::kPanelBytes + (((u % 8) ^ (row & 7)) << 4)),
                      "r"(q[4 * u]), "r"(q[4 * u + 1]), "r"(q[4 * u + 2]), "r"(q[4 * u + 3])
