@@ -109,11 +109,10 @@ struct Seq {
 };
 // The parts of one unit that this CTA joins
 struct Run {
-  int w0;               // the warp whose last part starts the unit (or, of a unit that
-                        // starts in an earlier CTA, whose first part is the first here)
-  unsigned mine;        // the warps whose first parts belong to it
-  int before, complete; // starts in an earlier CTA; starts and ends here
-  int q0, head, row0, nrows;
+  unsigned mine;         // the warps whose first parts belong to it
+  int w0;                // the warp whose last part starts the unit (or, of a unit that
+                         // starts in an earlier CTA, whose first part is the first here)
+  int before, complete;  // starts in an earlier CTA; starts and ends here
 };
 
 template <typename S>
@@ -125,7 +124,6 @@ struct Shared {
   // line summed over the warp that read them
   int4 seqs[S::kWarps * 32];
   Run runs[S::kWarps + 1];
-  int nruns;
   int cut[2];  // this CTA's stretch
   int abort;
   int last[2];
@@ -143,14 +141,17 @@ __device__ __forceinline__ Seq load_seq(const Fp4AttnParams& p, int s) {
   return make_seq<R>(p, q0, p.query_start_loc[s + 1] - q0, p.seq_lens[s]);
 }
 
-// a / b for 0 <= a, 0 < b, in a dozen instructions: code that a launch runs once
-// costs what its fetch costs.  The first quotient is off by at most 2^31 * 2^-22,
-// the second by one.
+// a / b for 0 <= a, 0 < b.  The first quotient is off by at most 2^31 * 2^-22, and
+// by one where a < 2^22; a second step brings the others there.
 __device__ __forceinline__ int divide(int a, int b) {
   const float inv = __fdividef(1.f, (float)b);
   int q = (int)((float)a * inv);
-  q += (int)((float)(a - q * b) * inv);
-  const int r = a - q * b;
+  int r = a - q * b;
+  if (a >= 1 << 22) {
+    const int more = (int)((float)r * inv);
+    q += more;
+    r -= more * b;
+  }
   return q + (r >= b) - (r < 0);
 }
 // query token of a row of a kv-head: row / group
@@ -172,7 +173,7 @@ struct Cursor {
     const int o = pos - pre;
     const int u = divide(o, q.nblk);
     blk = o - u * q.nblk;
-    head = divide(u, q.rgs);
+    head = q.rgs == 1 ? u : divide(u, q.rgs);
     rg = u - head * q.rgs;
     unit_start = pos - blk;
   }
@@ -242,13 +243,15 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
 
   // ---- the line of blocks (under 2^31 of them, which the host checks): its
   // length, this CTA's stretch of it and this warp's stretch of that, one step
-  // each.  Up to W * 32 sequences stay in shared memory between the steps (one
-  // barrier in all); more are gone over again in each.  Every warp searches
-  // the sums itself.
+  // each.  Up to W * 32 sequences stay in shared memory between the steps; more
+  // are gone over again in each.  What one warp can find out, one warp does:
+  // four warps share a scheduler, and all would wait for all of them.
   const bool resident = p.num_seqs <= W * 32;
   int per = 0, cta0 = 0, cta1 = 0;
   auto warp_start = [&](int w) { return cta0 + (int)((unsigned)(cta1 - cta0) * w / W); };
   Cursor<R> cu{};  // the arithmetic's
+  int upto = 0, from = 0;   // lane w: where warp w's sequences end and start on the line
+  int cost = 0, start = 0;  // of this thread's sequence: its blocks, and where they start
 #pragma unroll 1
   for (int step = 0; step < 3; ++step) {
     int base = 0;
@@ -257,7 +260,8 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
       if (step == 0 || !resident) {
         const int s = s0 + threadIdx.x;
         const Seq sq = s < p.num_seqs ? load_seq<R>(p, s) : Seq{};
-        int sum = sq.nblk * sq.rgs * p.num_kv_heads;
+        cost = sq.nblk * sq.rgs * p.num_kv_heads;
+        int sum = cost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int y = __shfl_up_sync(0xffffffffu, sum, o);
@@ -266,47 +270,48 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
         if (s0 > 0 || step > 0) __syncthreads();  // the ones before have been searched
         sh.seqs[threadIdx.x] = make_int4(sq.q0, sq.ql, sq.L, sum);
         __syncthreads();
-      }
-      // lane w: the blocks up to the end of warp w's sequences
-      int upto = lane < W ? sh.seqs[lane * 32 + 31].w : 0;
+        const int own = lane < W ? sh.seqs[lane * 32 + 31].w : 0;
+        upto = own;
 #pragma unroll
-      for (int o = 1; o < W; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
+        for (int o = 1; o < W; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+        upto += base;
+        from = upto - own;
+        start = __shfl_sync(0xffffffffu, from, warp) + sum - cost;
       }
-      upto += base;
-      // the sequence (of those in shared memory) that holds position `at`;
-      // *pre: where it starts
-      auto find = [&](int at, int* pre) {
-        const int w = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
-        const int before = w == 0 ? base : __shfl_sync(0xffffffffu, upto, w - 1);
-        const int end = sh.seqs[w * 32 + lane].w + before;
-        const int i = __ffs(__ballot_sync(0xffffffffu, end > at)) - 1;
-        const int up = __shfl_sync(0xffffffffu, end, max(i - 1, 0));
-        *pre = i == 0 ? before : up;
-        return w * 32 + i;
-      };
       const int end = __shfl_sync(0xffffffffu, upto, W - 1);
-      if (step == 1) {  // by the thread whose sequence holds the cut
-        const int4 q = sh.seqs[threadIdx.x];
-        const int mine = q.w + (warp == 0 ? base : __shfl_sync(0xffffffffu, upto, max(warp - 1, 0)));
-        const Seq sq = make_seq<R>(p, q.x, q.y, q.z);
-        const int start = mine - sq.nblk * sq.rgs * p.num_kv_heads;
+      // the sequence (of those in shared memory) that holds position `at`, and
+      // where it starts
+      auto find = [&](int at, Seq* sq, int* pre) {
+        const int w = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
+        const int before = __shfl_sync(0xffffffffu, from, w);
+        const int mine = sh.seqs[w * 32 + lane].w + before;
+        const int i = w * 32 + __ffs(__ballot_sync(0xffffffffu, mine > at)) - 1;
+        const int4 q = sh.seqs[i];
+        *sq = make_seq<R>(p, q.x, q.y, q.z);
+        *pre = q.w + before - sq->nblk * sq->rgs * p.num_kv_heads;
+        return i;
+      };
+      if (step == 1) {  // by the thread whose sequence holds the end of a stretch:
+        // moved to one of a short unit
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
-          const int at = min((long long)(blockIdx.x + i) * per, (long long)INT32_MAX);
-          if (at < start || at >= mine) continue;
-          const int r = at - start - divide(at - start, sq.nblk) * sq.nblk;
-          sh.cut[i] = sq.nblk > S::kWhole ? at : at + (2 * r < sq.nblk ? -r : sq.nblk - r);
+          const unsigned in = (blockIdx.x + i) * (unsigned)per - start;
+          if (in >= (unsigned)cost) continue;
+          const int nblk = (sh.seqs[threadIdx.x].z + kBlockSize - 1) / kBlockSize;
+          const int r = (int)in - divide((int)in, nblk) * nblk;
+          sh.cut[i] = start + (int)in + (nblk > S::kWhole ? 0 : 2 * r < nblk ? -r : nblk - r);
         }
       }
       if (step == 2) {
         const int at = warp_start(warp);
         if (at >= base && at < end) {
+          Seq sq;
           int pre;
-          const int i = find(at, &pre);
-          const int4 q = sh.seqs[i];
-          cu.begin(make_seq<R>(p, q.x, q.y, q.z), s0 + i, pre, at);
+          const int s = s0 + find(at, &sq, &pre);
+          cu.begin(sq, s, pre, at);
         }
       }
       base = end;
@@ -366,15 +371,14 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
       next0 = blk >= 0 ? ids[blk] : 0;
       next1 = both ? ids[blk + 1] : INT32_MIN;
     };
-    auto issue = [&]() {  // the next pair, if there is one
-      if (left == 0) {
-        if (next_pairs == 0) return;
-        left = next_pairs;
-        at_lane = 0;
-        tile0 = clamp_id(next0) * p.num_kv_heads + next_head;
-        tile1 = next1 == INT32_MIN ? -1 : clamp_id(next1) * p.num_kv_heads + next_head;
-        look_ahead();
-      }
+    auto install = [&]() {
+      left = next_pairs;
+      at_lane = 0;
+      tile0 = clamp_id(next0) * p.num_kv_heads + next_head;
+      tile1 = next1 == INT32_MIN ? -1 : clamp_id(next1) * p.num_kv_heads + next_head;
+      next_pairs = 0;
+    };
+    auto issue = [&]() {  // the next pair of the window
       if (lane == at_lane) {
         const uint32_t bar = bars + 8 * put, dst = ring + put * 2 * S::kTile;
         mbar_expect_tx(bar, tile1 < 0 ? S::kTile : 2 * S::kTile);
@@ -412,7 +416,10 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
       }
       if (first) {  // the first tiles' loads leave while the query's are under way
         look_ahead();
-        for (int i = 0; i < S::kStages; ++i) issue();
+        install();
+#pragma unroll 1
+        for (int i = 0; i < S::kStages && left > 0; ++i) issue();
+        if (ahead > 0) look_ahead();
         first = false;
       }
       uint32_t qf[QP][NT][K][2];
@@ -520,7 +527,11 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
           phase ^= 1;
         }
         __syncwarp();  // the stage is free once every lane holds its part of it
-        issue();
+        if (left == 0 && next_pairs > 0) {
+          install();
+          if (ahead > 0) look_ahead();
+        }
+        if (left > 0) issue();
 
         // -- S^T = K Q^T: scores in log2 units
         float x[2][NT][4];
@@ -712,54 +723,56 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
   __syncthreads();
   if (sh.abort) return;
 
-  // ---- join the parts: runs of parts of one unit, in order
-  if (warp == 0) {
-    const bool v0 = lane < W && sh.meta[lane % W][0].valid;
-    const bool v1 = lane < W && sh.meta[lane % W][1].valid;
-    const unsigned firsts = __ballot_sync(0xffffffffu, v0);
-    const unsigned starts = __ballot_sync(0xffffffffu, v1);
-    const unsigned ends = __ballot_sync(0xffffffffu, v0 && sh.meta[lane % W][0].ended);
-    // a unit from an earlier CTA: the first warp with a first part, if no unit
-    // starts in a warp before it
-    const int lead = firsts ? __ffs(firsts) - 1 : 31;
-    const bool carried = firsts && (starts & ((1u << lead) - 1)) == 0;
-    auto put = [&](bool before) {
-      unsigned mine = firsts & (~0u << (lane + (before ? 0 : 1)));
-      const unsigned end = ends & mine;
-      if (end) mine &= (end & -end) | ((end & -end) - 1);
-      const PartMeta& pm = sh.meta[lane][before ? 0 : 1];
-      sh.runs[before ? 0 : __popc(starts & ((1u << lane) - 1)) + carried] =
-          Run{lane, mine, before, end && !before, pm.q0, pm.head, pm.row0, pm.nrows};
-    };
-    if (v1) put(false);
-    if (carried && lane == lead) put(true);
-    if (lane == 0) sh.nruns = __popc(starts) + carried;
-  }
-  __syncthreads();
-  const int nruns = sh.nruns;
-  // a weight per (run, row) and part, written over the part's maximum
-  for (int i = threadIdx.x; i < nruns * R; i += W * 32) {
-    const Run& run = sh.runs[i / R];
-    const int row = i % R;
-    if (row >= run.nrows) continue;
-    const unsigned mine = run.mine;
-    float* start = sh.ml[run.w0][1][row];
-    float mx = -INFINITY, sum = 0.f;
-    auto for_each_part = [&](auto visit) {  // in the order of the keys
-      if (!run.before) visit(start);
-#pragma unroll 1
-      for (unsigned left = mine; left; left &= left - 1) visit(sh.ml[__ffs(left) - 1][0][row]);
-    };
-    for_each_part([&](const float* ml) { mx = fmaxf(mx, ml[0]); });
-    for_each_part([&](float* ml) {
-      const float wt = ml[0] == -INFINITY ? 0.f : ex2(ml[0] - mx);
-      sum = fmaf(wt, ml[1], sum);
-      ml[0] = wt;
-    });
-    if (run.complete) {
+  // ---- join the parts.  A run: the parts of one unit here, in order: the last
+  // part of the warp where it starts and first parts of the warps after it
+  // (slot w), or only first parts, of a unit that starts in an earlier CTA
+  // (slot W)
+  const bool v0 = lane < W && sh.meta[lane < W ? lane : 0][0].valid;
+  const bool v1 = lane < W && sh.meta[lane < W ? lane : 0][1].valid;
+  const unsigned firsts = __ballot_sync(0xffffffffu, v0);
+  const unsigned starts = __ballot_sync(0xffffffffu, v1);
+  const unsigned ends = __ballot_sync(0xffffffffu, v0 && sh.meta[lane < W ? lane : 0][0].ended);
+  // the first warp with a first part, if no unit starts in a warp before it
+  const int lead = firsts ? __ffs(firsts) - 1 : 31;
+  const bool carried = firsts && (starts & ((1u << lead) - 1)) == 0;
+  const int nruns = __popc(starts) + carried;
+  // a weight per run, row and part, written over the part's maximum
+  for (int i = threadIdx.x; i < (W + 1) * R; i += W * 32) {
+    const int slot = i / R, row = i % R;
+    const bool before = slot == W;
+    if (before ? !carried : !(starts >> slot & 1)) continue;
+    const int w0 = before ? lead : slot;
+    unsigned mine = firsts & (~0u << (before ? w0 : w0 + 1));
+    const unsigned end = ends & mine;
+    if (end) mine &= (end & -end) | ((end & -end) - 1);
+    const bool complete = end && !before;
+    if (row == 0)
+      sh.runs[before ? 0 : __popc(starts & ((1u << slot) - 1)) + carried] =
+          Run{mine, w0, before, complete};
+    if (row >= sh.meta[w0][before ? 0 : 1].nrows) continue;
+    // without branches: the lanes' runs differ (what a place holds that is not of
+    // the run is loaded and dropped)
+    float* start = sh.ml[w0][1][row];
+    float m[W + 1], sum = 0.f;
+    m[W] = before ? -INFINITY : start[0];
+    float mx = m[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      m[w] = mine >> w & 1 ? sh.ml[w][0][row][0] : -INFINITY;
+      mx = fmaxf(mx, m[w]);
+    }
+#pragma unroll
+    for (int w = 0; w <= W; ++w) {
+      float* ml = w < W ? sh.ml[w % W][0][row] : start;
+      const float wt = m[w] == -INFINITY ? 0.f : ex2(m[w] - mx);
+      const float l = ml[1];
+      sum += wt == 0.f ? 0.f : wt * l;
+      if (w < W ? mine >> w & 1 : !before) ml[0] = wt;
+    }
+    if (complete) {
       start[1] = p.v_scale / sum;  // (its own sum has been read)
     } else {
-      const int64_t at = (int64_t)(blockIdx.x * 2 + !run.before) * 16 + row;
+      const int64_t at = (int64_t)(blockIdx.x * 2 + !before) * 16 + row;
       *(float2*)(p.ws_ml + at * 2) = make_float2(mx, sum);
     }
   }
@@ -767,9 +780,10 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
   // four dims of a row per thread
   constexpr int kQuads = D / 4;
   for (int i = threadIdx.x; i < nruns * R * kQuads; i += W * 32) {
-    const Run& run = sh.runs[i / (R * kQuads)];
+    const Run run = sh.runs[i / (R * kQuads)];
+    const PartMeta& pm = sh.meta[run.w0][run.before ? 0 : 1];
     const int row = i / kQuads % R, off = row * D + i % kQuads * 4;
-    if (row >= run.nrows) continue;
+    if (row >= pm.nrows) continue;
     const unsigned mine = run.mine;
     float y[4] = {0.f, 0.f, 0.f, 0.f};
     auto add = [&](const unsigned char* part, float f) {
@@ -789,8 +803,8 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
       const float f = sh.ml[run.w0][1][row][1];
 #pragma unroll
       for (int k = 0; k < 4; ++k) y[k] *= f;
-      const int rr = run.row0 + row, j = token_of(p, rr);
-      store_dims<T>((T*)p.out + ((int64_t)(run.q0 + j) * p.num_q_heads + run.head * p.group +
+      const int rr = pm.row0 + row, j = token_of(p, rr);
+      store_dims<T>((T*)p.out + ((int64_t)(pm.q0 + j) * p.num_q_heads + pm.head * p.group +
                                  (rr - j * p.group)) * D + i % kQuads * 4,
                     y);
     } else {
