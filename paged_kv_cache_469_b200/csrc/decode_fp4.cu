@@ -89,10 +89,12 @@ struct Shape {
   static constexpr int ring_off = 0;
   static constexpr int part_off = ring_off + kWarps * kRing;  // first parts
   static constexpr int total = part_off + kWarps * kPart;
-  // Units up to this many blocks are not cut between CTAs: a cut costs the
-  // joining CTA two more round trips to memory (some 3 us), the stretches'
-  // unequal lengths at most this many blocks over the warps of a CTA
-  static constexpr int kWhole = 8 * kWarps;
+  // Units up to this many blocks are not cut between CTAs: joining a cut unit
+  // costs its CTA two more round trips to memory (3 to 5 us, by its rows), the
+  // unequal stretches at most this many blocks over the warps of a CTA.  64
+  // contexts of 128 .. 2048 at D = 64, 8 rows: 14.7 us, with half of it 17.0; 33
+  // of 40 .. 3000 with 13 drafted tokens, 16 rows: 18.7, with half of it 21.2.
+  static constexpr int kWhole = R * kWarps;
   static_assert(kStages >= 3 && kRing >= kPart, "a warp's last part takes its ring's place");
 };
 

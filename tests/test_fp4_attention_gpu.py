@@ -126,6 +126,104 @@ def test_long_contexts_over_many_processors(hq, hkv, d, lens):
         assert torch.equal(a, st.run())
 
 
+@pytest.mark.parametrize("lens,qls", [([300, 45, 517], [1, 200, 2]),  # (45: left out, its rows stay)
+                                      ([300, 245, 517], [1, 200, 2])])
+def test_offsets_past_32_bits(lens, qls):
+    """Blocks on both sides of 2 GB and 4 GB of a pool."""
+    st = Step(31, lens, qls, 8, 8, 128, junk=False)
+    want = st.run()
+    blocks = (9 << 29) // (8 * 18 * 128)  # 4.5 GB
+    rng = np.random.default_rng(2)
+    far = np.sort(rng.choice(blocks, st.pool.shape[0], replace=False)).astype(np.int32)
+    far[-1] = blocks - 1
+    big = torch.empty(blocks, 8, 18 * 128, dtype=torch.uint8, device="cuda")
+    big[torch.from_numpy(far).long().cuda()] = st.cache
+    st.cache = big
+    st.dev[0] = torch.from_numpy(np.where(st.tables >= 0, far[st.tables], -5)).int().cuda()
+    assert torch.equal(st.run().view(torch.int16), want.view(torch.int16))
+    slots = torch.from_numpy(far[::7].astype(np.int64) * 16 + 5).cuda()
+    k, v = lib.gather_fp4(big, slots, dtype=torch.float32)
+    kw, vw = fp4_side.tile_values(st.pool[::7], 128)
+    assert np.array_equal(k.cpu().numpy(), kw[:, :, 5].astype(np.float32))
+    assert np.array_equal(v.cpu().numpy(), vw[:, :, 5].astype(np.float32))
+    # rows appended there are found again
+    x = torch.randn(len(slots), 8, 128, device="cuda").bfloat16()
+    lib.rope_append_fp4(x[:, :0], x, x, big, slots, None, None)
+    small = lib.new_fp4_cache(len(slots), 8, 128)
+    lib.rope_append_fp4(x[:, :0], x, x, small, torch.arange(len(slots), device="cuda") * 16 + 5,
+                        None, None)
+    got = big[torch.from_numpy(far[::7]).long().cuda()]
+    keep = small != 0
+    assert torch.equal(got[keep], small[keep])
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured steps of different shape on one workspace, replayed in turn on one
+    stream, with an eager step between."""
+    a = Step(41, [3000, 200], [1, 1], 8, 2, 128)
+    b = Step(42, [90, 400, 17], [70, 400, 17], 8, 2, 128)
+    ws = lib.new_fp4_workspace(3, 487, 8, 2, 128)
+    a.ws = b.ws = ws
+    wants, graphs, outs = [], [], []
+    for st in (a, b):
+        wants.append(st.run())
+        outs.append(torch.empty_like(st.q))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            st.run(out=outs[-1])
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 0):
+        outs[i].fill_(float("nan"))
+        graphs[i].replay()
+        assert torch.equal(outs[i], wants[i])
+        assert torch.equal(b.run(host=True), wants[1])
+    a.check(outs[0])
+
+
+def test_a_nan_query_stays_in_its_row():
+    for dtype in ("bf16", "f32"):
+        st = Step(12, [150, 700], [100, 1], 8, 2, 64, dtype)
+        want = st.run()
+        st.q[5, 3, 7] = float("nan")
+        st.q[100, 2, 0] = float("inf")
+        got = st.run()
+        bad = torch.zeros_like(got, dtype=torch.bool)
+        bad[5, 3] = True
+        bad[100, 2] = True
+        assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], want[~bad])
+
+
+def test_a_prefix_shared_by_sequences_and_repeated_blocks():
+    st = Step(13, [400, 400, 64], [1, 90, 1], 8, 2, 128, junk=False)
+    st.tables[1, :10] = st.tables[0, :10]
+    st.tables[2] = st.tables[0, 3]  # one block four times over
+    st.dev[0] = torch.from_numpy(st.tables).cuda()
+    st.check(st.run())
+
+
+def test_lengths_beyond_the_bounds_are_left_out():
+    """A sequence longer than max_seq_len, or with more queries than keys, writes
+    nothing; its neighbours are right (to the bound: the step's lengths decide where
+    its keys are cut)."""
+    st = Step(14, [100, 50, 300], [1, 2, 1], 8, 2, 64, junk=False)
+    want = st.run()
+    st.dev[1].copy_(torch.tensor([100, 1, 300], dtype=torch.int32))
+    got = st.run()
+    assert torch.isnan(got[1:3]).all()
+    st.check(torch.cat([got[:1], want[1:3], got[3:]]))
+    st.dev[1].copy_(torch.tensor([301, 50, 300], dtype=torch.int32))
+    got = st.run()
+    assert torch.isnan(got[0]).all()
+    st.check(torch.cat([want[:1], got[1:]]))
+
+
+def test_no_sequence_has_work():
+    st = Step(15, [16, 0], [0, 0], 8, 2, 64, junk=False, extra_tokens=3)
+    out = torch.full_like(st.q, 2.0)
+    st.run(out=out)
+    assert (out == 2.0).all()
+
+
 def test_many_sequences():
     rng = np.random.default_rng(3)
     lens = rng.integers(0, 60, 1300)
