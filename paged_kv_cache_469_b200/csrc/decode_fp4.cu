@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
 }
 
 template <int D, int NT, int QP, typename T>
-cudaError_t launch_shape(const Fp4AttnParams& p, cudaStream_t stream) {
+cudaError_t launch_shape(const Fp4AttnParams& p, cudaStream_t stream, int max_ctas) {
   using S = Shape<D, NT, QP>;
   auto kernel = decode_fp4_kernel<S, T>;
   static std::atomic<int> smem_done[64];
@@ -893,7 +893,7 @@ cudaError_t launch_shape(const Fp4AttnParams& p, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(min(device_sm_count(), kFp4MaxCtas));
+  cfg.gridDim = dim3(min(min(device_sm_count(), kFp4MaxCtas), max_ctas));
   cfg.blockDim = dim3(S::kWarps * 32);
   cfg.dynamicSmemBytes = S::total;
   cfg.stream = stream;
@@ -905,22 +905,22 @@ cudaError_t launch_shape(const Fp4AttnParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_decode_fp4(const Fp4AttnParams& p, int head_dim, bool f32, int rows,
-                              cudaStream_t stream) {
+                              cudaStream_t stream, int max_ctas) {
   cudaError_t e;
   const bool wide = rows > 8;
   if (f32) {
     if (head_dim == 64)
-      e = wide ? launch_shape<64, 2, 2, float>(p, stream) : launch_shape<64, 1, 2, float>(p, stream);
+      e = wide ? launch_shape<64, 2, 2, float>(p, stream, max_ctas) : launch_shape<64, 1, 2, float>(p, stream, max_ctas);
     else
-      e = wide ? launch_shape<128, 2, 2, float>(p, stream)
-               : launch_shape<128, 1, 2, float>(p, stream);
+      e = wide ? launch_shape<128, 2, 2, float>(p, stream, max_ctas)
+               : launch_shape<128, 1, 2, float>(p, stream, max_ctas);
   } else {
     if (head_dim == 64)
-      e = wide ? launch_shape<64, 2, 1, __nv_bfloat16>(p, stream)
-               : launch_shape<64, 1, 1, __nv_bfloat16>(p, stream);
+      e = wide ? launch_shape<64, 2, 1, __nv_bfloat16>(p, stream, max_ctas)
+               : launch_shape<64, 1, 1, __nv_bfloat16>(p, stream, max_ctas);
     else
-      e = wide ? launch_shape<128, 2, 1, __nv_bfloat16>(p, stream)
-               : launch_shape<128, 1, 1, __nv_bfloat16>(p, stream);
+      e = wide ? launch_shape<128, 2, 1, __nv_bfloat16>(p, stream, max_ctas)
+               : launch_shape<128, 1, 1, __nv_bfloat16>(p, stream, max_ctas);
   }
   return e == cudaSuccess ? cudaGetLastError() : e;
 }

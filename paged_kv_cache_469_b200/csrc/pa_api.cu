@@ -53,6 +53,22 @@ WorkspaceLayout workspace_layout(int num_seqs, int num_q_heads, int num_kv_heads
   return w;
 }
 
+ForkStreams* fork_streams(cudaStream_t st) {
+  static thread_local ForkStreams per_dev[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  ForkStreams& f = per_dev[dev];
+  if (f.side && f.start && f.done) return &f;
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone)
+    return nullptr;
+  if ((!f.side && cudaStreamCreateWithFlags(&f.side, cudaStreamNonBlocking) != cudaSuccess) ||
+      (!f.start && cudaEventCreateWithFlags(&f.start, cudaEventDisableTiming) != cudaSuccess) ||
+      (!f.done && cudaEventCreateWithFlags(&f.done, cudaEventDisableTiming) != cudaSuccess))
+    return nullptr;
+  return &f;
+}
+
 }  // namespace pa
 
 using namespace pa;
@@ -161,31 +177,6 @@ namespace {
 // shortest step, 5e12 9 % longer, 6e12 16 % longer.
 constexpr double kPrefillFlopsPerSm = 3.7e12;
 constexpr double kDecodeBytesPerSm = 46.0e9;
-
-// A side stream and two events, per thread and device, for the calls that run
-// the prefill kernel beside the decode kernel.  Created on the first such call
-// outside a stream capture; a capture that would need to create them runs the
-// kernels one after the other instead.
-struct ForkStreams {
-  cudaStream_t side = nullptr;
-  cudaEvent_t start = nullptr, done = nullptr;
-};
-
-ForkStreams* fork_streams(cudaStream_t st) {
-  static thread_local ForkStreams per_dev[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-  ForkStreams& f = per_dev[dev];
-  if (f.side && f.start && f.done) return &f;
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone)
-    return nullptr;
-  if ((!f.side && cudaStreamCreateWithFlags(&f.side, cudaStreamNonBlocking) != cudaSuccess) ||
-      (!f.start && cudaEventCreateWithFlags(&f.start, cudaEventDisableTiming) != cudaSuccess) ||
-      (!f.done && cudaEventCreateWithFlags(&f.done, cudaEventDisableTiming) != cudaSuccess))
-    return nullptr;
-  return &f;
-}
 
 // The new tokens' K/V rows a call writes into the cache before it reads it
 // (pa_attention_varlen_write_cache); all null for pa_attention_varlen.
@@ -331,6 +322,7 @@ int attention_impl(void* out, const void* q, const void* k_cache, const void* v_
   p.ws_pieces = (int4*)(ws + w.pieces_off);
   p.ws_items = (int4*)(ws + w.items_off);
   p.max_items = w.max_items;
+  p.decode_max_rows = kDecodeMaxRows;
   if (fused_write) {
     p.k_new = cw.k_new;
     p.v_new = cw.v_new;

@@ -109,6 +109,82 @@ Fp4Workspace fp4_workspace(int num_seqs, int num_tokens, int num_q_heads, int he
   return w;
 }
 
+// Which kernel takes a sequence of ql query tokens: the decode kernel reads the
+// keys again for every 16 query rows, cuts them over all SMs and costs kBlockNs
+// per block and row group (GPU-wide); the prefill kernel takes 128 query tokens
+// of two heads at once on one SM, kTileNs per 128 keys.  Measured at 148 SMs.
+struct Fp4Costs {
+  double block_ns, tile_ns;
+  int even_q, odd_q;  // with every SM at work the kernels cost the same at about so
+                      // many query tokens: of two heads per item, of one
+};
+Fp4Costs fp4_costs(int head_dim) {
+  return head_dim == 128 ? Fp4Costs{0.60, 1950., 24, 44} : Fp4Costs{0.34, 1800., 36, 72};
+}
+constexpr double kLaunchNs = 8000.;  // a kernel's start and end
+
+// What fp4_split finds: the most query tokens of a sequence of the decode kernel,
+// and the two kernels' work in SM-nanoseconds.
+struct Fp4Split {
+  int decode_q;
+  double decode_sm_ns, prefill_sm_ns;
+};
+
+// Few prefill
+// items leave most SMs idle, whatever their length: one chunk of 64 tokens over
+// 32768 keys (32 + 8 heads of 128) takes 500 us there and 169 here.
+// Without the host copies a step is taken for one of equal lengths.
+Fp4Split fp4_split(int num_seqs, int num_tokens, int max_query_len, int max_seq_len,
+                 int num_q_heads, int num_kv_heads, int head_dim, const int32_t* seq_lens_host,
+                 const int32_t* query_start_loc_host) {
+  const int group = num_q_heads / num_kv_heads;
+  const Fp4Costs c = fp4_costs(head_dim);
+  const int base = group % 2 == 0 ? c.even_q : c.odd_q;
+  if (max_query_len <= base) return Fp4Split{base, 0., 0.};
+  // the candidates, and the step's sequences between one and the next
+  constexpr int kBins = 8;
+  const int most[kBins] = {base, 48, 96, 160, 256, 400, 640, INT32_MAX};
+  double blocks[kBins] = {}, tiles[kBins] = {}, longest[kBins] = {};
+  auto add = [&](int ql, int L, double times) {
+    int b = 0;
+    while (ql > most[b]) ++b;
+    const double kt = (L + kPrefillKvTile - 1) / kPrefillKvTile;
+    const int qt = (ql + kPrefillQTile - 1) / kPrefillQTile;
+    const double items = group % 2 == 0 ? qt * (num_q_heads / 2.) : (qt + 1) / 2 * (double)num_q_heads;
+    blocks[b] += times * ((L + kBlockSize - 1) / kBlockSize) *
+                 (((int64_t)ql * group + kDecodeRows - 1) / kDecodeRows) * num_kv_heads;
+    tiles[b] += times * items * kt;
+    longest[b] = max(longest[b], kt);
+  };
+  if (seq_lens_host && query_start_loc_host) {
+    for (int s = 0; s < num_seqs; ++s) {
+      const int ql = query_start_loc_host[s + 1] - query_start_loc_host[s];
+      if (ql > 0) add(ql, seq_lens_host[s], 1.);
+    }
+  } else {
+    const int n = max(1, min(num_seqs, num_tokens / max_query_len));
+    add(max_query_len, max_seq_len, n);
+  }
+  Fp4Split best{base, 0., 0.};
+  double best_ns = INFINITY, decode = 0.;
+  const int sms = device_sm_count();
+  for (int k = 0; k < kBins; ++k) {
+    decode += blocks[k];
+    double all = 0., far = 0.;
+    for (int j = k + 1; j < kBins; ++j) {
+      all += tiles[j];
+      far = max(far, longest[j]);
+    }
+    const double ns = (decode > 0. ? decode * c.block_ns + kLaunchNs : 0.) +
+                      (all > 0. ? max(all / sms, far) * c.tile_ns + kLaunchNs : 0.);
+    if (ns < best_ns) {
+      best_ns = ns;
+      best = Fp4Split{most[k], decode * c.block_ns * sms, all * c.tile_ns};
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 extern "C" int pa_rope_append(void* q_out, const void* q, int64_t q_stride, const void* k,
@@ -195,21 +271,31 @@ extern "C" int pa_attention_varlen_fp4(
   if (!aligned_to(out, 16) || !aligned_to(q, 16) || !aligned_to(kv_cache, 16) ||
       !aligned_to(block_tables, 4) || !aligned_to(seq_lens, 4) || !aligned_to(query_start_loc, 4))
     return PA_ERR_INVALID;
-  // ---- which kernels the step needs.  bf16 sequences of more than
-  // kDecodeMaxRows query rows per kv-head are the prefill kernel's
-  const bool f32 = dtype == PA_DTYPE_F32;
-  const int decode_q = f32 ? INT32_MAX : kDecodeMaxRows / group;  // most query tokens of the others
-  int longest = min(max_query_len, decode_q);                     // of the decode kernel's
-  bool any_decode = true, any_prefill = max_query_len > decode_q;
-  if (seq_lens_host && query_start_loc_host) {
+  const bool hints = seq_lens_host && query_start_loc_host;
+  if (hints) {
     if (query_start_loc_host[0] != 0 || query_start_loc_host[num_seqs] != num_tokens)
       return PA_ERR_INVALID;
-    longest = 0;
-    any_prefill = false;
     for (int s = 0; s < num_seqs; ++s) {
       const int ql = query_start_loc_host[s + 1] - query_start_loc_host[s];
       const int L = seq_lens_host[s];
       if (ql < 0 || ql > L || L > max_seq_len || ql > max_query_len) return PA_ERR_INVALID;
+    }
+  }
+  // ---- which kernels the step needs
+  const bool f32 = dtype == PA_DTYPE_F32;
+  const Fp4Split split =
+      f32 ? Fp4Split{INT32_MAX, 0., 0.}
+          : fp4_split(num_seqs, num_tokens, max_query_len, max_seq_len, num_q_heads, num_kv_heads,
+                      head_dim, hints ? seq_lens_host : nullptr,
+                      hints ? query_start_loc_host : nullptr);
+  const int decode_q = split.decode_q;  // most query tokens of a sequence of the decode kernel
+  int longest = min(max_query_len, decode_q);  // of the decode kernel's
+  bool any_decode = true, any_prefill = max_query_len > decode_q;
+  if (hints) {
+    longest = 0;
+    any_prefill = false;
+    for (int s = 0; s < num_seqs; ++s) {
+      const int ql = query_start_loc_host[s + 1] - query_start_loc_host[s];
       if (ql > decode_q)
         any_prefill = true;
       else
@@ -252,10 +338,13 @@ extern "C" int pa_attention_varlen_fp4(
   p.ws_counters = (int*)(ws + w.counters_off);
   p.ws_ml = (float*)(ws + w.ml_off);
   p.ws_o = (float*)(ws + w.o_off);
-  if (any_decode && launch_decode_fp4(p, head_dim, f32, (int)min(rows, (int64_t)INT32_MAX),
-                                      (cudaStream_t)stream) != cudaSuccess)
-    return PA_ERR_CUDA;
-  if (!any_prefill) return PA_OK;
+  const cudaStream_t st = (cudaStream_t)stream;
+  const int sms = device_sm_count();
+  auto run_decode = [&](int ctas) {
+    return launch_decode_fp4(p, head_dim, f32, (int)min(rows, (int64_t)INT32_MAX), st, ctas) ==
+           cudaSuccess;
+  };
+  if (!any_prefill) return !any_decode || run_decode(sms) ? PA_OK : PA_ERR_CUDA;
   AttnParams a{};
   a.out = out;
   a.q = q;
@@ -275,8 +364,23 @@ extern "C" int pa_attention_varlen_fp4(
   a.ws_status = a.ws_header = p.ws_status;
   a.ws_items = (int4*)(ws + w.items_off);
   a.max_items = w.max_items;
-  return launch_prefill_fp4(a, v_scale, head_dim, max_query_len, seq_lens_host,
-                            query_start_loc_host, (cudaStream_t)stream) == cudaSuccess
-             ? PA_OK
-             : PA_ERR_CUDA;
+  a.decode_max_rows = (int)min((int64_t)decode_q * group, (int64_t)INT32_MAX);
+  auto run_prefill = [&](cudaStream_t on, int ctas) {
+    return launch_prefill_fp4(a, v_scale, head_dim, max_query_len, seq_lens_host,
+                              query_start_loc_host, on, ctas) == cudaSuccess;
+  };
+  // both kinds of work, known from the host copies: side by side, each on the
+  // SMs of its share, since one is bound by the cache's bytes and the other is not
+  ForkStreams* fork = hints && any_decode ? fork_streams(st) : nullptr;
+  if (!fork)
+    return (!any_decode || run_decode(sms)) && run_prefill(st, sms) ? PA_OK : PA_ERR_CUDA;
+  const double share = split.prefill_sm_ns / (split.prefill_sm_ns + split.decode_sm_ns);
+  const int prefill_ctas = max(1, min((int)lround(sms * share), sms - 1));
+  if (cudaEventRecord(fork->start, st) != cudaSuccess ||
+      cudaStreamWaitEvent(fork->side, fork->start, 0) != cudaSuccess ||
+      !run_prefill(fork->side, prefill_ctas) || !run_decode(sms - prefill_ctas) ||
+      cudaEventRecord(fork->done, fork->side) != cudaSuccess ||
+      cudaStreamWaitEvent(st, fork->done, 0) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return PA_OK;
 }

@@ -120,7 +120,8 @@ struct AttnParams {
   int* ws_status;    // the workspace header (kWs* words); [0]: error bits
   int* ws_header;    // = ws_status
   int4* ws_pieces;   // device-built decode piece list
-  // prefill work list
+  // prefill work list: of sequences with more query rows per kv-head than this
+  int decode_max_rows;
   int4* ws_items;    // prefill items (seq, q-tile, q-head, kv tiles)
   int max_items;
 };
@@ -142,6 +143,16 @@ struct DecodeWork {
 
 // bits of ws_status[0]
 constexpr int kStatusWaitTimeout = 1;  // an mbarrier wait exceeded its time limit
+
+// A side stream and two events, per thread and device, for the calls that run
+// the prefill kernel beside the decode kernel.  Created on the first such call
+// outside a stream capture; a capture that would need to create them runs the
+// kernels one after the other instead.
+struct ForkStreams {
+  cudaStream_t side = nullptr;
+  cudaEvent_t start = nullptr, done = nullptr;
+};
+ForkStreams* fork_streams(cudaStream_t st);
 
 // Workspace layout shared by the size query and the launch.
 struct WorkspaceLayout {
@@ -208,8 +219,9 @@ struct Fp4AttnParams {
 };
 constexpr int kFp4MaxCtas = 256;
 // `rows`: most query rows per kv-head of a sequence the kernel takes.
+// At most max_ctas CTAs.
 cudaError_t launch_decode_fp4(const Fp4AttnParams& p, int head_dim, bool f32, int rows,
-                              cudaStream_t stream);
+                              cudaStream_t stream, int max_ctas);
 
 // Rows of a 4-bit cache as values (pa_gather_fp4).
 struct GatherFp4Params {
@@ -251,7 +263,8 @@ cudaError_t launch_prefill_tcgen05(const AttnParams& p, int head_dim, int max_qu
 // The same over a 4-bit cache (p.k_cache): p.scale_log2 holds its k_scale.
 cudaError_t launch_prefill_fp4(const AttnParams& p, float v_scale, int head_dim,
                                int max_query_len, const int32_t* seq_lens_host,
-                               const int32_t* query_start_loc_host, cudaStream_t stream);
+                               const int32_t* query_start_loc_host, cudaStream_t stream,
+                               int max_ctas);
 
 // pa_attention_varlen without the side stream of a mixed step (the two
 // classes run one after the other): for the caller that must not create any

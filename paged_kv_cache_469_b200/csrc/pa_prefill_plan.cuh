@@ -70,7 +70,7 @@ prefill_plan_kernel(const AttnParams p, int max_tiles, int pair_heads) {
   // pass 1: histogram of items by tile count
   for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
     const int q0 = p.query_start_loc[s], ql = p.query_start_loc[s + 1] - q0, L = p.seq_lens[s];
-    if (ql * p.group <= kDecodeMaxRows || ql > L) continue;
+    if (ql * p.group <= p.decode_max_rows || ql > L) continue;
     const int nq = (ql + QT - 1) / QT;
     const int ni = pair_heads ? nq : (nq + 1) / 2;
     for (int i = 0; i < ni; ++i) {
@@ -94,7 +94,7 @@ prefill_plan_kernel(const AttnParams p, int max_tiles, int pair_heads) {
   // pass 2: scatter
   for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
     const int q0 = p.query_start_loc[s], ql = p.query_start_loc[s + 1] - q0, L = p.seq_lens[s];
-    if (ql * p.group <= kDecodeMaxRows || ql > L) continue;
+    if (ql * p.group <= p.decode_max_rows || ql > L) continue;
     const int nq = (ql + QT - 1) / QT;
     const int ni = pair_heads ? nq : (nq + 1) / 2;
     for (int i = ni - 1; i >= 0; --i) {
@@ -125,7 +125,7 @@ bool host_work_list(PrefillWork* work, const AttnParams& p, const int32_t* seq_l
     for (int s = 0; s < p.num_seqs; ++s) {
       const int ql = query_start_loc_host[s + 1] - query_start_loc_host[s];
       const int L = seq_lens_host[s];
-      if (ql * p.group <= kDecodeMaxRows || ql > L) continue;
+      if (ql * p.group <= p.decode_max_rows || ql > L) continue;
       const int nq = (ql + QT - 1) / QT;
       const int ni = pair_heads ? nq : (nq + 1) / 2;
       for (int i = 0; i < ni; ++i) {

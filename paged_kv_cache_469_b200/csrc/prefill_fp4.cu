@@ -716,7 +716,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
 template <int D>
 cudaError_t launch_d(const AttnParams& p, float v_scale, int max_query_len,
                      const int32_t* seq_lens_host, const int32_t* query_start_loc_host,
-                     cudaStream_t stream) {
+                     cudaStream_t stream, int max_ctas) {
   CUtensorMap tq;
   if (!make_map(&tq, p.q, D, p.num_q_heads, p.num_tokens, (uint64_t)D * 2,
                 (uint64_t)p.num_q_heads * D * 2, 1, QT))
@@ -736,7 +736,7 @@ cudaError_t launch_d(const AttnParams& p, float v_scale, int max_query_len,
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(max(1, min(device_sm_count(), upper)));
+  cfg.gridDim = dim3(max(1, min(min(device_sm_count(), max_ctas), upper)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -749,12 +749,13 @@ cudaError_t launch_d(const AttnParams& p, float v_scale, int max_query_len,
 
 cudaError_t launch_prefill_fp4(const AttnParams& p, float v_scale, int head_dim,
                                int max_query_len, const int32_t* seq_lens_host,
-                               const int32_t* query_start_loc_host, cudaStream_t stream) {
+                               const int32_t* query_start_loc_host, cudaStream_t stream,
+                               int max_ctas) {
   cudaError_t e = head_dim == 64
                       ? launch_d<64>(p, v_scale, max_query_len, seq_lens_host,
-                                     query_start_loc_host, stream)
+                                     query_start_loc_host, stream, max_ctas)
                       : launch_d<128>(p, v_scale, max_query_len, seq_lens_host,
-                                      query_start_loc_host, stream);
+                                      query_start_loc_host, stream, max_ctas);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

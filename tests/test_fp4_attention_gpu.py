@@ -116,6 +116,49 @@ def test_prompt_chunks(hq, hkv, d, dtype, lens, qls):
     st.check(st.run(host=True))
 
 
+def tensor_core_work(qls, lens, hq, hkv, d):
+    """(ns of the chunks on the prefill kernel, ns on the decode kernel), by the rates
+    that the library chooses with."""
+    block_ns, tile_ns = (0.60, 1950.0) if d == 128 else (0.34, 1800.0)
+    group = hq // hkv
+    tiles = decode = longest = 0.0
+    for q, n in zip(qls, lens):
+        qt = -(-q // 128)
+        items = qt * hq / 2 if group % 2 == 0 else -(-qt // 2) * hq
+        tiles += items * -(-n // 128)
+        longest = max(longest, -(-n // 128))
+        decode += -(-n // 16) * -(-q * group // 16) * hkv * block_ns
+    return max(tiles / 148, longest) * tile_ns, decode
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (32, 4, 64), (24, 8, 128), (32, 2, 64)])
+def test_chunks_on_the_tensor_cores(hq, hkv, d):
+    """Enough chunks that they run on the prefill kernel: lengths around its tiles of
+    128 queries and 128 keys, with and without context, between decodes."""
+    qls = [128, 129, 127, 256, 300, 1, 200, 131, 255, 1, 257, 140, 128, 384, 130, 190]
+    lens = [128, 129, 300, 511, 300, 77, 513, 640, 255, 900, 270, 141, 1024, 385, 131, 700]
+    chunks = [(q, n) for q, n in zip(qls, lens) if q > 1]
+    tensor, decode = tensor_core_work(*zip(*chunks), hq, hkv, d)
+    assert tensor + 16000 < decode, "the case is too small to reach the prefill kernel"
+    st = Step(hq + d, lens, qls, hq, hkv, d)
+    out = st.run(host=True)
+    st.check(out)
+    st.check(st.run())  # lengths known on the device only
+    assert torch.equal(st.run(host=True), out)
+    # a NaN or an infinity stays in its row
+    st.q[300, 3, 9], st.q[5, 1, 0] = float("nan"), float("inf")
+    got = st.run(host=True)
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[300, 3] = bad[5, 1] = True
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], out[~bad])
+    # query rows behind the last sequence (without host copies, which would refuse them)
+    st = Step(hq + d, lens, qls, hq, hkv, d, extra_tokens=2)
+    out = torch.full_like(st.q, 9.0)
+    st.run(out=out)
+    st.check(out)
+    assert (out[-2:] == 9.0).all()
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (8, 1, 64), (16, 1, 128)])
 @pytest.mark.parametrize("lens", [[20011], [9000, 3, 12000], [16 * 148 * 16], [16 * 148 * 16 + 1]])
 def test_long_contexts_over_many_processors(hq, hkv, d, lens):
@@ -127,7 +170,8 @@ def test_long_contexts_over_many_processors(hq, hkv, d, lens):
 
 
 @pytest.mark.parametrize("lens,qls", [([300, 45, 517], [1, 200, 2]),  # (45: left out, its rows stay)
-                                      ([300, 245, 517], [1, 200, 2])])
+                                      ([300, 245, 517], [1, 200, 2]),
+                                      ([400] * 24, [250] * 24)])  # (on the tensor cores)
 def test_offsets_past_32_bits(lens, qls):
     """Blocks on both sides of 2 GB and 4 GB of a pool."""
     st = Step(31, lens, qls, 8, 8, 128, junk=False)
