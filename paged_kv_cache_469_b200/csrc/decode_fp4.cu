@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
       }
 
       float o[NT][K][4];
-      float m[NT][2], l[NT][2];
+      float m[NT][2], l[NT][2], base[NT][2];  // (base: what an exponent adds, 7 - m)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
 #pragma unroll
           for (int c = 0; c < 4; ++c) o[n][i][c] = 0.f;
         m[n][0] = m[n][1] = -INFINITY;
-        l[n][0] = l[n][1] = 0.f;
+        l[n][0] = l[n][1] = base[n][0] = base[n][1] = 0.f;
       }
 
       // -- two blocks at a time (the second of the last pair may be none: its
@@ -535,15 +535,15 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
         }
         if (left > 0) issue();
 
-        // -- S^T = K Q^T: scores in log2 units
+        // -- S^T = K Q^T (one chain of MMAs per block and row tile: a second
+        // costs its sums, 138.8 against 132.2 us for 256 contexts of 8192 at D 64)
         float x[2][NT][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float sc[NT][2][4];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sc[n][0][c] = sc[n][1][c] = 0.f;
+            for (int c = 0; c < 4; ++c) x[i][n][c] = 0.f;
           __half2 k2[2][2];  // [token][group of the chunk]
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -563,13 +563,9 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int qp = 0; qp < QP; ++qp)
-                  mma_f16(sc[n][j], a[0][2 * j], a[1][2 * j], a[0][2 * j + 1], a[1][2 * j + 1],
+                  mma_f16(x[i][n], a[0][2 * j], a[1][2 * j], a[0][2 * j + 1], a[1][2 * j + 1],
                           qf[qp][n][2 * w + j][0], qf[qp][n][2 * w + j][1]);
           }
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) x[i][n][c] = (sc[n][0][c] + sc[n][1][c]) * sl2[n][c & 1];
         }
         // -- keys past a row's last visible one are out
         const int key0 = (blk0 + b) * kBlockSize;
@@ -587,14 +583,14 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
             if (held < 4) vs[i] = held <= 0 ? 0u : vs[i] & (0xffffffffu >> (32 - 8 * held));
           }
         }
-        // -- the running max moves when a score passes it by 2^8
+        // -- the running max (in log2 units) moves when a score passes it by 2^8
         float mx[NT][2];
         bool over = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            mx[n][c] = fmaxf(fmaxf(x[0][n][c], x[0][n][c + 2]), fmaxf(x[1][n][c], x[1][n][c + 2]));
+            mx[n][c] = sl2[n][c] * fmaxf(max3(x[0][n][c], x[0][n][c + 2], x[1][n][c]), x[1][n][c + 2]);
             // (a max of -inf is passed by every score but -inf)
             over |= mx[n][c] > m[n][c] + kRescale;
           }
@@ -609,6 +605,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
               if (v > m[n][c] + kRescale) {
                 const float f = ex2(m[n][c] - v);
                 m[n][c] = v;
+                base[n][c] = kPShift - v;
                 l[n][c] *= f;
 #pragma unroll
                 for (int i = 0; i < K; ++i) {
@@ -622,16 +619,16 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
         uint32_t pf[2][QP][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float base[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) base[c] = m[n][c] == -INFINITY ? 0.f : m[n][c] - kPShift;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float e[4];
+            const uint64_t sc2 = f2(sl2[n][0], sl2[n][1]), ba2 = f2(base[n][0], base[n][1]);
+            f2_split(fma2(f2(x[i][n][0], x[i][n][1]), sc2, ba2), e[0], e[1]);
+            f2_split(fma2(f2(x[i][n][2], x[i][n][3]), sc2, ba2), e[2], e[3]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) e[c] = ex2(x[i][n][c] - base[c & 1]);
-            l[n][0] += e[0] + e[2];
-            l[n][1] += e[1] + e[3];
+            for (int c = 0; c < 4; ++c) e[c] = ex2(e[c]);
+            f2_split(add2(f2(l[n][0], l[n][1]), add2(f2(e[0], e[1]), f2(e[2], e[3]))), l[n][0],
+                     l[n][1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const __half2 hi = __floats2half2_rn(e[2 * h], e[2 * h + 1]);
