@@ -45,7 +45,9 @@ namespace pa {
 namespace {
 
 constexpr int kTileBlocks = KT / kBlockSize;    // 8 cache blocks per tile
-constexpr int kStages = 2;                      // K tiles, and V tiles
+// K and V tiles.  V(t) is needed a round after K(t), and the stages of both free
+// up together at a round's end: with two K stages the next K tile was late.
+constexpr int kKStages = 3, kVStages = 2;
 constexpr int kThreads = 512;                   // 16 warps = 4 warpgroups
 // Six producers: 8, 10, 11, 12, 14, 15.  Four chunks of 1024 over 2712 .. 5048
 // tokens: 358 us with three producers in 384 threads (a producer warp is bound
@@ -71,8 +73,8 @@ struct Layout {
   static constexpr int kBytes = kPanels * kPanelBytes;  // one Q, K or V tile
   static constexpr int q_off = 0;                   // two Q tiles (the two halves)
   static constexpr int k_off = q_off + 2 * kBytes;
-  static constexpr int v_off = k_off + kStages * kBytes;
-  static constexpr int bar_off = v_off + kStages * kBytes;
+  static constexpr int v_off = k_off + kKStages * kBytes;
+  static constexpr int bar_off = v_off + kVStages * kBytes;
   static constexpr int used = bar_off + 256;
   // one CTA per SM (its tensor memory is all of the SM's)
   static constexpr int total = (used < 120 * 1024 ? 120 * 1024 : used) + 1024;
@@ -85,10 +87,10 @@ enum : int {
   kBarQReady,                       // and are f16
   kBarQEmpty,
   kBarKFull,                        // + stage
-  kBarKEmpty = kBarKFull + kStages,
-  kBarVFull = kBarKEmpty + kStages,
-  kBarVEmpty = kBarVFull + kStages,
-  kBarSFull = kBarVEmpty + kStages,  // + half
+  kBarKEmpty = kBarKFull + kKStages,
+  kBarVFull = kBarKEmpty + kKStages,
+  kBarVEmpty = kBarVFull + kVStages,
+  kBarSFull = kBarVEmpty + kVStages,  // + half
   kBarPFull = kBarSFull + 2,
   kBarODone = kBarPFull + 2,
   kBarItem = kBarODone + 2,          // + ring slot of items
@@ -301,9 +303,11 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
     mbar_init(bar(kBarQFull), 1);
     mbar_init(bar(kBarQReady), 8);  // one arrival per softmax warp
     mbar_init(bar(kBarQEmpty), 1);
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kKStages; ++i) {
       mbar_init(bar(kBarKFull + i), kProducers);
       mbar_init(bar(kBarKEmpty + i), 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
       mbar_init(bar(kBarVFull + i), kProducers);
       mbar_init(bar(kBarVEmpty + i), 1);
     }
@@ -405,14 +409,15 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         }
         nxt.next(p, work, num_items, item_at);
         ids_n = nxt.ids(p, lane);
-        const int st = g % kStages;
         const int key0 = cur.t * KT;
 #pragma unroll
         for (int phase = 0; phase < 2 && ok; ++phase) {
+          const uint32_t nst = phase ? kVStages : kKStages;
+          const int st = g % nst;
           const int full = (phase ? kBarVFull : kBarKFull) + st;
           const int empty = (phase ? kBarVEmpty : kBarKEmpty) + st;
-          if (g >= kStages) {
-            ok = wait_bar(bar(empty), ((g / kStages) - 1) & 1, abort_flag, status);
+          if (g >= nst) {
+            ok = wait_bar(bar(empty), ((g / nst) - 1) & 1, abort_flag, status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
@@ -457,7 +462,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         if (!ok) return;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t dv = dv0 + (uint64_t)(((gt % kStages) * LY::kBytes) >> 4);
+          const uint64_t dv = dv0 + (uint64_t)(((gt % kVStages) * LY::kBytes) >> 4);
           const uint32_t dst = tmem + kTmemO + 128 * h;
           const uint32_t pa = tmem + kTmemS + 128 * h;
 #pragma unroll
@@ -470,7 +475,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       };
       auto issue_qk = [&](int h, uint32_t gt) {  // S_h = Q_h K^T (tile gt)
         if (elect_one()) {
-          const uint64_t dk = dk0 + (uint64_t)(((gt % kStages) * LY::kBytes) >> 4);
+          const uint64_t dk = dk0 + (uint64_t)(((gt % kKStages) * LY::kBytes) >> 4);
           const uint64_t dq = dq0 + (uint64_t)((h * LY::kBytes) >> 4);
           const uint32_t dst = tmem + kTmemS + 128 * h;
 #pragma unroll
@@ -489,9 +494,9 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         ok = wait_bar(bar(kBarQReady), k & 1, abort_flag, status);
         const uint32_t g_first = g;
         for (int t = 0; t < it.ntiles && ok; ++t, ++g) {
-          ok = wait_bar(bar(kBarKFull + g % kStages), (g / kStages) & 1, abort_flag, status);
+          ok = wait_bar(bar(kBarKFull + g % kKStages), (g / kKStages) & 1, abort_flag, status);
           if (ok && t > 0)
-            ok = wait_bar(bar(kBarVFull + (g - 1) % kStages), ((g - 1) / kStages) & 1, abort_flag,
+            ok = wait_bar(bar(kBarVFull + (g - 1) % kVStages), ((g - 1) / kVStages) & 1, abort_flag,
                           status);
           if (!ok) break;
           tc_fence_after();
@@ -500,18 +505,18 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
             if (ok) issue_qk(h, g);
           }
           if (ok && elect_one()) {
-            umma_commit(bar(kBarKEmpty + g % kStages));
-            if (t > 0) umma_commit(bar(kBarVEmpty + (g - 1) % kStages));
+            umma_commit(bar(kBarKEmpty + g % kKStages));
+            if (t > 0) umma_commit(bar(kBarVEmpty + (g - 1) % kVStages));
             if (t == it.ntiles - 1) umma_commit(bar(kBarQEmpty));
           }
           __syncwarp();
         }
         if (ok && it.ntiles > 0) {  // P.V of the item's last tile
           const uint32_t gl = g - 1;
-          ok = wait_bar(bar(kBarVFull + gl % kStages), (gl / kStages) & 1, abort_flag, status);
+          ok = wait_bar(bar(kBarVFull + gl % kVStages), (gl / kVStages) & 1, abort_flag, status);
           if (ok) tc_fence_after();
           for (int h = 0; h < 2 && ok; ++h) issue_pv(h, gl, gl == g_first);
-          if (ok && elect_one()) umma_commit(bar(kBarVEmpty + gl % kStages));
+          if (ok && elect_one()) umma_commit(bar(kBarVEmpty + gl % kVStages));
           __syncwarp();
         }
       }
