@@ -1,10 +1,11 @@
-"""Build libpa.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc.
+"""Build libpa.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc, and the
+Python module ``_binding`` (argument marshalling) with g++.
 
     python -m paged_kv_cache_469_b200.build [--force]
 
 Objects go to ``paged_kv_cache_469_b200/_build/``; the shared library to
-``paged_kv_cache_469_b200/libpa.so``.  Sources are recompiled when they (or
-the headers) are newer than their object.
+``paged_kv_cache_469_b200/libpa.so``, the module beside it.  Sources are
+recompiled when they (or the headers) are newer than their object.
 """
 from __future__ import annotations
 
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -52,11 +54,38 @@ def _compile(src: str, force: bool, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _binding(force: bool) -> str:
+    """The Python module, against the installed torch's headers and libraries."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, "binding.cpp")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "pa.h")))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    root = os.path.dirname(torch.__file__)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-I", INCLUDE,
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", "/usr/local/cuda/include",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+           "-ldl"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        module = ex.submit(_binding, force)
         objs = list(ex.map(lambda s: _compile(s, force, verbose_ptxas), srcs))
+        module.result()
     if (force or not os.path.exists(LIB)
             or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs)):
         tmp = LIB + f".tmp{os.getpid()}"

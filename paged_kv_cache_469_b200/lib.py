@@ -1,4 +1,5 @@
-"""Python binding of libpa.so: argument marshalling only.
+"""Python binding of libpa.so: argument marshalling only (ctypes; the module
+``_binding`` for the calls that a decode step makes many times).
 
 Every call forwards torch tensors' device pointers and the current CUDA
 stream to the C ABI declared in ``include/pa.h``; every step of the
@@ -263,94 +264,22 @@ def plan_step(free_queue: torch.Tensor, planner_state: torch.Tensor,
         raise PAError(rc, "pa_plan_step")
 
 
-FP4_BLOCK_SIZE = 16  # tokens of a block, and so of a 4-bit tile
+_native = None
 
 
-# The calls below are often bound by the host (a decode step's kernels take a few
-# microseconds): their checks are plain expressions, and name the offender only
-# once one has failed.
-
-def _refuse_devices(**tensors) -> None:
-    first, dev = next((n, t.get_device()) for n, t in tensors.items())
-    for name, t in tensors.items():
-        if t.get_device() < 0 or t.get_device() != dev:
-            raise ValueError(f"{name} must be a CUDA tensor, on the device of {first}")
-
-
-def _refuse_strided(**tensors) -> None:
-    for name, t in tensors.items():
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-
-
-def _call(name, dev: int, stream, *args) -> None:
-    """The C call ``name`` on ``stream`` (None: the current one of device ``dev``), with
-    that device current."""
-    fn = getattr(library(), name)
-    if dev == torch._C._cuda_getDevice():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
-                else stream.cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _stream(stream))
-    if rc != PA_OK:
-        raise PAError(rc, name)
-
-
-def _rows(t: torch.Tensor, name: str, tokens: int, heads: int, d: int) -> int:
-    """Elements from one token's row to the next of a [tokens][heads][d] tensor
-    whose rows are contiguous (a slice of a fused projection, for instance)."""
-    row, head, one = t.stride()
-    if (head != d and heads > 1) or (one != 1 and d > 1):
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}] with contiguous rows")
-    return row if tokens > 1 else heads * d
-
-
-def _append(name, q, k, v, caches, scales, slot_mapping, positions, cos_sin, q_out, interleaved,
-            hkv, d, num_blocks, stream) -> torch.Tensor:
-    """Both appends: the checks they share, and the call."""
-    t, hq, _ = q.shape
-    if q_out is None:
-        q_out = torch.empty(t, hq, d, dtype=q.dtype, device=q.device)
-    dt = k.dtype
-    if q.dtype != dt or v.dtype != dt or q_out.dtype != dt:
-        raise TypeError("q, k, v and q_out must have one dtype")
-    if slot_mapping.dtype != torch.int64:
-        raise TypeError("slot_mapping must be int64")
-    rows = (t, hkv, d)
-    if k.shape != rows or v.shape != rows or q.shape != (t, hq, d) or q_out.shape != q.shape or \
-            slot_mapping.shape != (t,):
-        raise ValueError("the sizes of q, k, v, q_out, slot_mapping and the cache do not fit")
-    dev = k.get_device()
-    if dev < 0 or q.get_device() != dev or v.get_device() != dev or \
-            q_out.get_device() != dev or slot_mapping.get_device() != dev or \
-            caches[0].get_device() != dev or caches[-1].get_device() != dev:
-        _refuse_devices(k=k, q=q, v=v, q_out=q_out, slot_mapping=slot_mapping, cache=caches[0],
-                        v_cache=caches[-1])
-    if not (q_out.is_contiguous() and slot_mapping.is_contiguous() and
-            caches[0].is_contiguous() and caches[-1].is_contiguous()):
-        _refuse_strided(q_out=q_out, slot_mapping=slot_mapping, cache=caches[0],
-                        v_cache=caches[-1])
-    rotary, longest, pos_ptr, cs_ptr = 0, 0, None, None
-    if cos_sin is not None:
-        if positions is None or positions.dtype != torch.int64:
-            raise TypeError("positions must be int64")
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
-            raise TypeError("cos_sin must be a float32 [max_position, rotary_dim] tensor")
-        if positions.shape != (t,):
-            raise ValueError("inconsistent size of positions")
-        if positions.get_device() != dev or cos_sin.get_device() != dev:
-            _refuse_devices(k=k, positions=positions, cos_sin=cos_sin)
-        if not (positions.is_contiguous() and cos_sin.is_contiguous()):
-            _refuse_strided(positions=positions, cos_sin=cos_sin)
-        longest, rotary = cos_sin.shape
-        pos_ptr, cs_ptr = positions.data_ptr(), cos_sin.data_ptr()
-    _call(name, dev, stream, q_out.data_ptr(), q.data_ptr(), _rows(q, "q", t, hq, d),
-          k.data_ptr(), _rows(k, "k", t, hkv, d), v.data_ptr(), _rows(v, "v", t, hkv, d),
-          *[c.data_ptr() for c in caches], *scales, slot_mapping.data_ptr(), pos_ptr, cs_ptr,
-          longest, rotary, int(interleaved), t, hq, hkv, d, FP4_BLOCK_SIZE, num_blocks,
-          _dtype_code(k))
-    return q_out
+def _marshal():
+    """The module ``_binding`` (built in-tree like the library), bound to the library."""
+    global _native
+    if _native is None:
+        library()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(f"the module _binding is missing ({e}): build it with "
+                               "`python -m paged_kv_cache_469_b200.build`") from e
+        _binding.load(LIB_PATH)
+        _native = _binding
+    return _native
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -366,14 +295,13 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torc
     positions: int64 [T]; cos_sin: float32 [max_position, rotary_dim], the
     cosines and then the sines of a position's angles (None: nothing is
     rotated).  Returns q_out (a new tensor unless given)."""
-    num_blocks, hkv, bs, d = k_cache.shape
-    if bs != FP4_BLOCK_SIZE or v_cache.shape != k_cache.shape:
-        raise ValueError("rope_append: the caches' shapes do not fit")
-    if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
-        raise TypeError("the caches must have the dtype of k")
-    return _append("pa_rope_append", q, k, v, (k_cache, v_cache), (),
-                   slot_mapping, positions, cos_sin, q_out, interleaved, hkv, d, num_blocks,
-                   stream)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    rc = _marshal().rope_append(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out,
+                                interleaved, None if stream is None else stream.cuda_stream)
+    if rc != PA_OK:
+        raise PAError(rc, "pa_rope_append")
+    return q_out
 
 
 def new_fp4_cache(num_blocks: int, num_kv_heads: int, head_dim: int,
@@ -383,13 +311,6 @@ def new_fp4_cache(num_blocks: int, num_kv_heads: int, head_dim: int,
     return torch.zeros(num_blocks, num_kv_heads, 18 * head_dim, dtype=torch.uint8, device=device)
 
 
-def _fp4_cache(kv_cache: torch.Tensor):
-    num_blocks, hkv, tile = kv_cache.shape
-    if kv_cache.dtype != torch.uint8 or tile % 18:
-        raise TypeError("kv_cache must be uint8 [num_blocks, num_kv_heads, 18 * head_dim]")
-    return num_blocks, hkv, tile // 18
-
-
 def rope_append_fp4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_cache: torch.Tensor,
                     slot_mapping: torch.Tensor, positions: torch.Tensor | None,
                     cos_sin: torch.Tensor | None, *, k_scale: float = 1.0, v_scale: float = 1.0,
@@ -397,10 +318,14 @@ def rope_append_fp4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_cache:
                     stream=None) -> torch.Tensor:
     """``rope_append`` into a 4-bit cache (see pa_rope_append_fp4 in pa.h); k_scale and
     v_scale are the tensors' own scales."""
-    num_blocks, hkv, d = _fp4_cache(kv_cache)
-    return _append("pa_rope_append_fp4", q, k, v, (kv_cache,),
-                   (float(k_scale), float(v_scale)), slot_mapping, positions, cos_sin, q_out,
-                   interleaved, hkv, d, num_blocks, stream)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    rc = _marshal().rope_append_fp4(q, k, v, kv_cache, k_scale, v_scale, slot_mapping, positions,
+                                    cos_sin, q_out, interleaved,
+                                    None if stream is None else stream.cuda_stream)
+    if rc != PA_OK:
+        raise PAError(rc, "pa_rope_append_fp4")
+    return q_out
 
 
 def gather_fp4(kv_cache: torch.Tensor, slots: torch.Tensor, *, k_scale: float = 1.0,
@@ -408,27 +333,16 @@ def gather_fp4(kv_cache: torch.Tensor, slots: torch.Tensor, *, k_scale: float = 
                v_out: torch.Tensor | None = None, stream=None):
     """K and V values ([n, Hkv, D] each) of the slots (int64 [n]) of a 4-bit cache; rows
     of slots outside the pool are left as they are (see pa_gather_fp4 in pa.h)."""
-    num_blocks, hkv, d = _fp4_cache(kv_cache)
-    n = slots.shape[0]
-    if slots.dtype != torch.int64:
-        raise TypeError("slots must be int64")
-    if k_out is None:
-        k_out = torch.zeros(n, hkv, d, dtype=dtype, device=kv_cache.device)
-    if v_out is None:
-        v_out = torch.zeros(n, hkv, d, dtype=k_out.dtype, device=kv_cache.device)
-    if k_out.shape != (n, hkv, d) or v_out.shape != (n, hkv, d):
-        raise ValueError("gather_fp4: k_out and v_out must be [n, num_kv_heads, head_dim]")
-    if v_out.dtype != k_out.dtype:
-        raise TypeError("k_out and v_out must have one dtype")
-    dev = kv_cache.get_device()
-    if dev < 0 or not (slots.get_device() == k_out.get_device() == v_out.get_device() == dev):
-        _refuse_devices(kv_cache=kv_cache, slots=slots, k_out=k_out, v_out=v_out)
-    if not (kv_cache.is_contiguous() and slots.is_contiguous() and k_out.is_contiguous() and
-            v_out.is_contiguous()):
-        _refuse_strided(kv_cache=kv_cache, slots=slots, k_out=k_out, v_out=v_out)
-    _call("pa_gather_fp4", dev, stream, k_out.data_ptr(), v_out.data_ptr(), kv_cache.data_ptr(),
-          float(k_scale), float(v_scale), slots.data_ptr(), n, hkv, d, FP4_BLOCK_SIZE, num_blocks,
-          _dtype_code(k_out))
+    if k_out is None or v_out is None:
+        shape = (slots.shape[0], kv_cache.shape[1], kv_cache.shape[2] // 18)
+        if k_out is None:
+            k_out = torch.zeros(shape, dtype=dtype, device=kv_cache.device)
+        if v_out is None:
+            v_out = torch.zeros(shape, dtype=k_out.dtype, device=kv_cache.device)
+    rc = _marshal().gather_fp4(kv_cache, slots, k_scale, v_scale, k_out, v_out,
+                               None if stream is None else stream.cuda_stream)
+    if rc != PA_OK:
+        raise PAError(rc, "pa_gather_fp4")
     return k_out, v_out
 
 
@@ -442,14 +356,17 @@ def new_fp4_workspace(num_seqs: int, num_tokens: int, num_q_heads: int, num_kv_h
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     if not ws.is_cuda:
         raise ValueError("the workspace must be on a CUDA device")
-    _call("pa_workspace_init", ws.get_device(), stream, ws.data_ptr(), n)
+    with torch.cuda.device(ws.device):
+        rc = library().pa_workspace_init(ws.data_ptr(), n, _stream(stream))
+    if rc != PA_OK:
+        raise PAError(rc, "pa_workspace_init")
     return ws
 
 
 def _host_lengths(a, n: int):
-    """(pointer, keep-alive) of n host lengths, or (None, None)."""
+    """(address, keep-alive) of n host lengths, or (0, None)."""
     if a is None:
-        return None, None
+        return 0, None
     if isinstance(a, torch.Tensor):
         a = a.cpu().numpy()
     if not (isinstance(a, np.ndarray) and a.dtype == np.int32 and a.flags.c_contiguous):
@@ -467,35 +384,14 @@ def attention_varlen_fp4(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Ten
                          stream=None) -> torch.Tensor:
     """Paged attention of one flattened step over a 4-bit cache (see
     pa_attention_varlen_fp4 in pa.h)."""
-    num_blocks, hkv, d = _fp4_cache(kv_cache)
-    t, hq, qd = q.shape
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or \
-            query_start_loc.dtype != torch.int32:
-        raise TypeError("block_tables, seq_lens and query_start_loc must be int32")
-    if out.dtype != q.dtype:
-        raise TypeError("out must have the dtype of q")
     s = seq_lens.shape[0]
-    if qd != d or out.shape != q.shape or block_tables.shape[0] != s or \
-            query_start_loc.shape[0] != s + 1:
-        raise ValueError("attention_varlen_fp4: inconsistent sizes")
-    dev = q.get_device()
-    if dev < 0 or not (out.get_device() == kv_cache.get_device() == block_tables.get_device() ==
-                       seq_lens.get_device() == query_start_loc.get_device() ==
-                       workspace.get_device() == dev):
-        _refuse_devices(q=q, out=out, kv_cache=kv_cache, block_tables=block_tables,
-                        seq_lens=seq_lens, query_start_loc=query_start_loc, workspace=workspace)
-    if not (out.is_contiguous() and q.is_contiguous() and kv_cache.is_contiguous() and
-            block_tables.is_contiguous() and seq_lens.is_contiguous() and
-            query_start_loc.is_contiguous() and workspace.is_contiguous()):
-        _refuse_strided(q=q, out=out, kv_cache=kv_cache, block_tables=block_tables,
-                        seq_lens=seq_lens, query_start_loc=query_start_loc, workspace=workspace)
     sl_ptr, sl_keep = _host_lengths(seq_lens_host, s)
     qs_ptr, qs_keep = _host_lengths(query_start_loc_host, s + 1)
-    _call("pa_attention_varlen_fp4", dev, stream, out.data_ptr(), q.data_ptr(),
-          kv_cache.data_ptr(), float(k_scale), float(v_scale), block_tables.data_ptr(),
-          block_tables.shape[1], seq_lens.data_ptr(), query_start_loc.data_ptr(), s, t,
-          max_query_len, max_seq_len, hq, hkv, d, FP4_BLOCK_SIZE, num_blocks, float(scale),
-          _dtype_code(q), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-          sl_ptr, qs_ptr)
+    rc = _marshal().attention_varlen_fp4(
+        out, q, kv_cache, k_scale, v_scale, block_tables, seq_lens, query_start_loc,
+        max_query_len, max_seq_len, scale, workspace, sl_ptr, qs_ptr,
+        None if stream is None else stream.cuda_stream)
     del sl_keep, qs_keep
+    if rc != PA_OK:
+        raise PAError(rc, "pa_attention_varlen_fp4")
     return out
