@@ -440,10 +440,21 @@ size_t pa_attention_fp4_workspace_size(int num_seqs, int num_tokens, int num_q_h
  * with K, V the cache's values, and everything else as there (positions, heads,
  * block tables, bounds).  Slots of the last block past seq_lens[s] are never
  * used, whatever they hold; a block id outside the pool is never dereferenced.
- * dtype is that of q and out.  The host copies are optional; the kernels plan
- * the step's work from the device arrays, so a captured call follows those.
+ * dtype is that of q and out, which must not overlap.  The kernels plan the
+ * step's work from the device arrays; the optional host copies are checked, and
+ * decide which kernels run and on how many SMs: a captured call without them
+ * follows whatever lengths the device arrays hold at its replay, one with them
+ * needs query lengths of the same sequences.
+ *
+ * A sequence of few query tokens (by a rule on the step's sizes; all of an fp32
+ * step) runs on a split-K kernel that reads the cache once per kv-head and 16
+ * query rows, over all SMs; longer prompt chunks run on a tensor-core kernel.
+ * The keys of a sequence are cut by the lengths of the whole step: equal steps
+ * give equal bits, other companions may change a result's last bits.
  * Supported: head_dim in {64, 128}; block_size 16; num_q_heads a multiple of
- * num_kv_heads with at most 16 q-heads per kv-head; dtype f32 or bf16.
+ * num_kv_heads with at most 16 q-heads per kv-head; dtype f32 or bf16; fewer than
+ * 2^31 blocks, counted once per sequence, kv-head and 16 query rows (8 where no
+ * sequence has more) of the split-K kernel, at max_seq_len each.
  */
 int pa_attention_varlen_fp4(void* out, const void* q, const void* kv_cache, float k_scale,
                             float v_scale, const int32_t* block_tables, int max_blocks_per_seq,

@@ -30,6 +30,7 @@
 // The query goes in as f16 too, each row times a power of two that brings its
 // largest value into [1, 2): bf16's eight bits fit; fp32 queries and their
 // probabilities are split into two f16 terms each, 22 bits in all.
+#include <float.h>
 #include <math.h>
 
 #include "pa_fastmath.cuh"
@@ -469,7 +470,8 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int er = __shfl_sync(0xffffffffu, e, (2 * t + c) * 4);
-          sl2[n][c] = p.scale_log2 * exp2i(er);
+          // (a scale below the smallest normal number would make NaN of a masked score)
+          sl2[n][c] = fmaxf(p.scale_log2 * exp2i(er), FLT_MIN);
           const int r2 = cu.rg * R + n * 8 + 2 * t + c;
           lim[n][c] = n * 8 + 2 * t + c < nrows ? cu.q.L - cu.q.ql + token_of(p, r2) : cu.q.L - 1;
         }

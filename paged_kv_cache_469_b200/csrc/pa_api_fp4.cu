@@ -271,6 +271,12 @@ extern "C" int pa_attention_varlen_fp4(
   if (!aligned_to(out, 16) || !aligned_to(q, 16) || !aligned_to(kv_cache, 16) ||
       !aligned_to(block_tables, 4) || !aligned_to(seq_lens, 4) || !aligned_to(query_start_loc, 4))
     return PA_ERR_INVALID;
+  // a unit's rows are read by several CTAs while others write theirs
+  {
+    const size_t bytes = (size_t)num_tokens * num_q_heads * head_dim *
+                         (dtype == PA_DTYPE_F32 ? 4 : 2);
+    if (Range{out, bytes}.overlaps(Range{q, bytes})) return PA_ERR_INVALID;
+  }
   const bool hints = seq_lens_host && query_start_loc_host;
   if (hints) {
     if (query_start_loc_host[0] != 0 || query_start_loc_host[num_seqs] != num_tokens)

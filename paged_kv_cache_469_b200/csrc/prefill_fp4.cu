@@ -31,6 +31,7 @@
 // Every mbarrier wait is bounded by a time limit; a wait that runs out sets a
 // status bit in the workspace and the CTA winds down instead of hanging.
 #include <cuda.h>
+#include <float.h>
 #include <math.h>
 
 #include "pa_fastmath.cuh"
@@ -553,7 +554,8 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         top = max(top, max(q[i] & 0x7fffu, q[i] >> 16 & 0x7fffu));
       const int e = min(max((int)(top >> 7) - 127, -126), 126);
       const float f = exp2i(-e);
-      sl2_next = p.scale_log2 * exp2i(e);
+      // (a scale below the smallest normal number would make NaN of a masked score)
+      sl2_next = fmaxf(p.scale_log2 * exp2i(e), FLT_MIN);
 #pragma unroll
       for (int u = 0; u < D / 8; ++u) {
 #pragma unroll

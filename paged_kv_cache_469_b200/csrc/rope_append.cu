@@ -101,8 +101,8 @@ __device__ __forceinline__ uint32_t group_scale(float amax, float six_g) {
 }
 // eight codes under that scale, dim 2j in the low half of byte j
 __device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t scale, float g) {
-  const float s = e4m3_to_float(scale);
-  const float d = s > 0.f ? __fmul_rn(s, g) : INFINITY;
+  const float product = __fmul_rn(e4m3_to_float(scale), g);
+  const float d = product > 0.f ? product : INFINITY;
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)

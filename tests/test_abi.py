@@ -240,9 +240,9 @@ def test_gather_fp4_argument_checks(L):
 
 
 def _fp4(L, **kw):
-    args = dict(out=16, q=16, kv=16, gk=1.0, gv=1.0, bt=16, mb=8, sl=16, qsl=16, S=1, T=1, mq=1,
-                ms=16, hq=8, hkv=2, d=64, bs=16, nb=4, scale=0.125, dt=1, ws=0, wsb=0, slh=None,
-                qslh=None, stream=None)
+    args = dict(out=1 << 40, q=16, kv=16, gk=1.0, gv=1.0, bt=16, mb=8, sl=16, qsl=16, S=1, T=1,
+                mq=1, ms=16, hq=8, hkv=2, d=64, bs=16, nb=4, scale=0.125, dt=1, ws=0, wsb=0,
+                slh=None, qslh=None, stream=None)
     args.update(kw)
     return L.pa_attention_varlen_fp4(*args.values())
 
@@ -268,3 +268,19 @@ def test_fp4_attention_argument_checks(L):
     assert _fp4(L, S=-1) == palib.PA_ERR_INVALID
     assert _fp4(L, T=0) == palib.PA_OK
     assert _fp4(L) == palib.PA_ERR_INVALID          # no workspace
+    big = 1 << 24                                   # workspace bytes, never touched below
+    assert _fp4(L, out=16, ws=16, wsb=big) == palib.PA_ERR_INVALID          # out is q
+    assert _fp4(L, out=16 + 512, T=2, ws=16, wsb=big) == palib.PA_ERR_INVALID  # overlaps q
+    # host copies that contradict the scalars
+    import numpy as np
+    sl, ok, bad = (np.array(x, np.int32) for x in ([4], [0, 1], [0, 5]))
+    assert _fp4(L, T=5, mq=5, slh=sl.ctypes.data, qslh=bad.ctypes.data, ws=16, wsb=big) == \
+        palib.PA_ERR_INVALID
+    assert _fp4(L, T=2, slh=sl.ctypes.data, qslh=ok.ctypes.data, ws=16, wsb=big) == \
+        palib.PA_ERR_INVALID
+    # more blocks than the decode kernel's line counts; more key tiles than the
+    # prefill plan's counters
+    assert _fp4(L, S=16384, T=16384, hq=64, hkv=16, ms=1 << 18, mb=1 << 14, ws=16, wsb=1) == \
+        palib.PA_ERR_UNSUPPORTED
+    assert _fp4(L, T=4096, mq=4096, ms=8 << 20, mb=1 << 19, ws=16, wsb=1) == \
+        palib.PA_ERR_UNSUPPORTED

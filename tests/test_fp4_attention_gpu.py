@@ -285,6 +285,13 @@ def test_extreme_scores(spread, q_spread, dtype):
     st.check(st.run())
 
 
+@pytest.mark.parametrize("scale", [1e-38, 1e-30, 30.0])
+def test_vanishing_and_large_scales(scale):
+    st = Step(6, [700, 90, 100] + [300] * 14, [1, 70, 2] + [200] * 14, 32, 8, 64, q_spread=1e-3)
+    st.scale = scale
+    st.check(st.run())
+
+
 def test_rows_behind_the_last_sequence_stay():
     st = Step(8, [50, 200, 33], [1, 100, 2], 8, 2, 64, extra_tokens=9)
     out = torch.full_like(st.q, 5.0)
@@ -376,6 +383,16 @@ def test_binding_refusals():
                 dict(seq_lens_host=np.array([21], np.int32), query_start_loc_host=st.qsl)):
         with pytest.raises(lib.PAError):
             st.run(**bad)
+    with pytest.raises(lib.PAError):
+        st.run(out=st.q)
+    keep = st.q
+    for q in (keep.cpu(), keep[:, :4], keep[..., ::2]):
+        st.q = q
+        with pytest.raises(ValueError):
+            st.run(out=torch.empty_like(keep))
+    st.q = keep
+    with pytest.raises(TypeError):
+        st.run(out=torch.empty_like(keep, dtype=torch.float32))
     st.cache = st.cache[..., :1000].contiguous()
     with pytest.raises(TypeError):
         st.run()
