@@ -109,52 +109,71 @@ Fp4Workspace fp4_workspace(int num_seqs, int num_tokens, int num_q_heads, int he
   return w;
 }
 
-// Which kernel takes a sequence of ql query tokens: the decode kernel reads the
-// keys again for every 16 query rows, cuts them over all SMs and costs kBlockNs
-// per block and row group (GPU-wide); the prefill kernel takes 128 query tokens
-// of two heads at once on one SM, kTileNs per 128 keys.  Measured at 148 SMs.
+// What the two attention kernels cost, measured at 148 SMs.  The decode kernel
+// reads the keys again for every 16 query rows (8 where no sequence has more) and
+// spreads them over all SMs; the prefill kernel takes 128 query tokens of two
+// heads at once, an item, on one SM.
 struct Fp4Costs {
-  double block_ns, tile_ns;
-  int even_q, odd_q;  // with every SM at work the kernels cost the same at about so
-                      // many query tokens: of two heads per item, of one
+  double block_ns[2];  // SM-nanoseconds per block and group of 8, of 16 rows
+  double tile_ns;      // per item and 128 keys
+  int even_q, odd_q;   // with every SM at work the kernels cost the same at about so
+                       // many query tokens: where the heads pair up, where they do not
 };
 Fp4Costs fp4_costs(int head_dim) {
-  return head_dim == 128 ? Fp4Costs{0.60, 1950., 24, 44} : Fp4Costs{0.34, 1800., 36, 72};
+  return head_dim == 128 ? Fp4Costs{{60., 93.}, 1950., 24, 44} : Fp4Costs{{38., 50.}, 1800., 36, 72};
 }
 constexpr double kLaunchNs = 8000.;  // a kernel's start and end
 
-// What fp4_split finds: the most query tokens of a sequence of the decode kernel,
-// and the two kernels' work in SM-nanoseconds.
+// The prefill kernel's work of a step.
+struct PrefillLoad {
+  double items = 0., tiles = 0., longest = 0.;
+  // its time on n SMs: the items are given out heaviest first
+  double ns(int n, double tile_ns) const {
+    if (items <= 0.) return 0.;
+    return tile_ns * (items <= n ? longest : max(longest, tiles / n + longest / 2)) + kLaunchNs;
+  }
+};
 struct Fp4Split {
-  int decode_q;
-  double decode_sm_ns, prefill_sm_ns;
+  int decode_q;         // most query tokens of a sequence of the decode kernel
+  double decode_sm_ns;  // its work
+  PrefillLoad prefill;
+  double decode_ns(int n) const {
+    return decode_sm_ns > 0. ? decode_sm_ns / n + kLaunchNs : 0.;
+  }
 };
 
-// Few prefill
-// items leave most SMs idle, whatever their length: one chunk of 64 tokens over
-// 32768 keys (32 + 8 heads of 128) takes 500 us there and 169 here.
-// Without the host copies a step is taken for one of equal lengths.
+// Divides a step's sequences between the kernels by their query tokens.  Few
+// prefill items leave most SMs idle, whatever their length: one chunk of 64 tokens
+// over 32768 keys (32 + 8 heads of 128) takes 500 us there and 169 here.  Without
+// the host copies a step is taken for one of equal lengths.
 Fp4Split fp4_split(int num_seqs, int num_tokens, int max_query_len, int max_seq_len,
-                 int num_q_heads, int num_kv_heads, int head_dim, const int32_t* seq_lens_host,
-                 const int32_t* query_start_loc_host) {
+                   int num_q_heads, int num_kv_heads, int head_dim, const int32_t* seq_lens_host,
+                   const int32_t* query_start_loc_host) {
   const int group = num_q_heads / num_kv_heads;
+  const bool paired = group % 2 == 0;
   const Fp4Costs c = fp4_costs(head_dim);
-  const int base = group % 2 == 0 ? c.even_q : c.odd_q;
-  if (max_query_len <= base) return Fp4Split{base, 0., 0.};
+  const int base = paired ? c.even_q : c.odd_q;
+  if (max_query_len <= base) return Fp4Split{base, 0., {}};
   // the candidates, and the step's sequences between one and the next
   constexpr int kBins = 8;
   const int most[kBins] = {base, 48, 96, 160, 256, 400, 640, INT32_MAX};
-  double blocks[kBins] = {}, tiles[kBins] = {}, longest[kBins] = {};
+  double blocks[kBins][2] = {};  // block reads in groups of 8, of 16 rows
+  int rows[kBins] = {};
+  PrefillLoad load[kBins];
   auto add = [&](int ql, int L, double times) {
     int b = 0;
     while (ql > most[b]) ++b;
     const double kt = (L + kPrefillKvTile - 1) / kPrefillKvTile;
+    const double nblk = times * ((L + kBlockSize - 1) / kBlockSize) * num_kv_heads;
     const int qt = (ql + kPrefillQTile - 1) / kPrefillQTile;
-    const double items = group % 2 == 0 ? qt * (num_q_heads / 2.) : (qt + 1) / 2 * (double)num_q_heads;
-    blocks[b] += times * ((L + kBlockSize - 1) / kBlockSize) *
-                 (((int64_t)ql * group + kDecodeRows - 1) / kDecodeRows) * num_kv_heads;
-    tiles[b] += times * items * kt;
-    longest[b] = max(longest[b], kt);
+    const double items = times * (paired ? qt * (num_q_heads / 2.) : (qt + 1) / 2 * (double)num_q_heads);
+    const int64_t r = (int64_t)ql * group;
+    blocks[b][0] += nblk * ((r + 7) / 8);
+    blocks[b][1] += nblk * ((r + 15) / 16);
+    rows[b] = max(rows[b], (int)min(r, (int64_t)64));
+    load[b].items += items;
+    load[b].tiles += items * kt;
+    load[b].longest = max(load[b].longest, kt);
   };
   if (seq_lens_host && query_start_loc_host) {
     for (int s = 0; s < num_seqs; ++s) {
@@ -162,24 +181,44 @@ Fp4Split fp4_split(int num_seqs, int num_tokens, int max_query_len, int max_seq_
       if (ql > 0) add(ql, seq_lens_host[s], 1.);
     }
   } else {
-    const int n = max(1, min(num_seqs, num_tokens / max_query_len));
-    add(max_query_len, max_seq_len, n);
+    add(max_query_len, max_seq_len, max(1, min(num_seqs, num_tokens / max_query_len)));
   }
-  Fp4Split best{base, 0., 0.};
-  double best_ns = INFINITY, decode = 0.;
   const int sms = device_sm_count();
+  Fp4Split best{base, 0., {}};
+  double best_ns = INFINITY, reads[2] = {0., 0.};
+  int most_rows = 0;
   for (int k = 0; k < kBins; ++k) {
-    decode += blocks[k];
-    double all = 0., far = 0.;
+    reads[0] += blocks[k][0];
+    reads[1] += blocks[k][1];
+    most_rows = max(most_rows, rows[k]);
+    const int wide = most_rows > 8;
+    Fp4Split s{most[k], reads[wide] * c.block_ns[wide], {}};
     for (int j = k + 1; j < kBins; ++j) {
-      all += tiles[j];
-      far = max(far, longest[j]);
+      s.prefill.items += load[j].items;
+      s.prefill.tiles += load[j].tiles;
+      s.prefill.longest = max(s.prefill.longest, load[j].longest);
     }
-    const double ns = (decode > 0. ? decode * c.block_ns + kLaunchNs : 0.) +
-                      (all > 0. ? max(all / sms, far) * c.tile_ns + kLaunchNs : 0.);
+    const double ns = s.decode_ns(sms) + s.prefill.ns(sms, c.tile_ns);
     if (ns < best_ns) {
       best_ns = ns;
-      best = Fp4Split{most[k], decode * c.block_ns * sms, all * c.tile_ns};
+      best = s;
+    }
+  }
+  return best;
+}
+
+// SMs for the prefill kernel when both run side by side, each on its own; 0 where
+// that is not expected to end sooner than one after the other.
+int fp4_prefill_sms(const Fp4Split& s, int head_dim) {
+  const double tile_ns = fp4_costs(head_dim).tile_ns;
+  const int sms = device_sm_count();
+  double best_ns = 0.95 * (s.decode_ns(sms) + s.prefill.ns(sms, tile_ns));
+  int best = 0;
+  for (int n = 4; n < sms; n += 4) {
+    const double ns = max(s.prefill.ns(n, tile_ns), s.decode_ns(sms - n));
+    if (ns < best_ns) {
+      best_ns = ns;
+      best = n;
     }
   }
   return best;
@@ -290,7 +329,7 @@ extern "C" int pa_attention_varlen_fp4(
   // ---- which kernels the step needs
   const bool f32 = dtype == PA_DTYPE_F32;
   const Fp4Split split =
-      f32 ? Fp4Split{INT32_MAX, 0., 0.}
+      f32 ? Fp4Split{INT32_MAX, 0., {}}
           : fp4_split(num_seqs, num_tokens, max_query_len, max_seq_len, num_q_heads, num_kv_heads,
                       head_dim, hints ? seq_lens_host : nullptr,
                       hints ? query_start_loc_host : nullptr);
@@ -309,7 +348,11 @@ extern "C" int pa_attention_varlen_fp4(
     }
     any_decode = longest > 0;
   }
-  const int64_t rows = (int64_t)longest * group;
+  // query rows per kv-head that choose the decode kernel's row group: where prompt
+  // chunks are in the step and lengths are not known, the rest is taken for
+  // one-token decodes (192 of them and 4 chunks of 512: 358 -> 279 us; any length
+  // is computed right by either group)
+  const int64_t rows = (int64_t)(any_prefill && !hints ? 1 : longest) * group;
   // the prefill plan keeps a counter per 128-key tile in shared memory
   if (any_prefill && max_blocks_per_seq / (kPrefillKvTile / kBlockSize) > 50000)
     return PA_ERR_UNSUPPORTED;
@@ -375,13 +418,12 @@ extern "C" int pa_attention_varlen_fp4(
     return launch_prefill_fp4(a, v_scale, head_dim, max_query_len, seq_lens_host,
                               query_start_loc_host, on, ctas) == cudaSuccess;
   };
-  // both kinds of work, known from the host copies: side by side, each on the
-  // SMs of its share, since one is bound by the cache's bytes and the other is not
-  ForkStreams* fork = hints && any_decode ? fork_streams(st) : nullptr;
+  // both kinds of work, known from the host copies: side by side, since one is
+  // bound by the cache's bytes and the other by arithmetic
+  const int prefill_ctas = hints && any_decode ? fp4_prefill_sms(split, head_dim) : 0;
+  ForkStreams* fork = prefill_ctas > 0 ? fork_streams(st) : nullptr;
   if (!fork)
     return (!any_decode || run_decode(sms)) && run_prefill(st, sms) ? PA_OK : PA_ERR_CUDA;
-  const double share = split.prefill_sm_ns / (split.prefill_sm_ns + split.decode_sm_ns);
-  const int prefill_ctas = max(1, min((int)lround(sms * share), sms - 1));
   if (cudaEventRecord(fork->start, st) != cudaSuccess ||
       cudaStreamWaitEvent(fork->side, fork->start, 0) != cudaSuccess ||
       !run_prefill(fork->side, prefill_ctas) || !run_decode(sms - prefill_ctas) ||

@@ -396,3 +396,27 @@ def test_binding_refusals():
     st.cache = st.cache[..., :1000].contiguous()
     with pytest.raises(TypeError):
         st.run()
+
+
+def test_mixed_step_side_by_side_is_joined_to_the_stream():
+    """Decodes and chunks with host copies may run on two streams: work queued after the
+    call sees every row, and a second call on the workspace starts after it."""
+    qls = [1] * 40 + [200] * 10
+    lens = [900 + 37 * i for i in range(40)] + [200 + 51 * i for i in range(10)]
+    st = Step(77, lens, qls, 32, 8, 128, junk=False)
+    want = st.run()
+    st.check(want)
+    out = torch.empty_like(st.q)
+    copies = []
+    for _ in range(3):
+        out.fill_(float("nan"))
+        st.run(host=True, out=out)
+        copies.append(out.clone())
+    st.check(copies[0])
+    assert torch.equal(copies[0], copies[1]) and torch.equal(copies[0], copies[2])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        st.run(host=True, out=out)
+    out.fill_(float("nan"))
+    g.replay()
+    assert torch.equal(out, copies[0])
