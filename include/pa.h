@@ -454,7 +454,11 @@ size_t pa_attention_fp4_workspace_size(int num_seqs, int num_tokens, int num_q_h
  * Supported: head_dim in {64, 128}; block_size 16; num_q_heads a multiple of
  * num_kv_heads with at most 16 q-heads per kv-head; dtype f32 or bf16; fewer than
  * 2^31 blocks, counted once per sequence, kv-head and 16 query rows (8 where no
- * sequence has more) of the split-K kernel, at max_seq_len each.
+ * sequence has more) of the split-K kernel, at max_seq_len each; with chunks for the
+ * tensor-core kernel, max_blocks_per_seq up to 400007.
+ * A NaN in a sequence's K row reaches the query rows that see that key.  One in a V
+ * row may reach earlier rows of the same chunk too (a masked key's weight is 0, and
+ * 0 times NaN is NaN), never another sequence's.
  */
 int pa_attention_varlen_fp4(void* out, const void* q, const void* kv_cache, float k_scale,
                             float v_scale, const int32_t* block_tables, int max_blocks_per_seq,

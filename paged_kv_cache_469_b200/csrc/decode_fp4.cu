@@ -28,8 +28,16 @@
 //   O^T += V^T P^T  P in f16, 2^7 times itself so that its small values keep
 //                 their bits (at most 2^15), transposed in registers
 // The query goes in as f16 too, each row times a power of two that brings its
-// largest value into [1, 2): bf16's eight bits fit; fp32 queries and their
-// probabilities are split into two f16 terms each, 22 bits in all.
+// largest value into [1, 2): bf16's eight bits fit (of values under 2^-14 of the
+// largest, those above 2^-25 of it); fp32 queries and their probabilities are split
+// into two f16 terms each, 22 bits in all.
+//
+// Bound: the cache's bytes and the instructions that convert them, together.  192
+// contexts of 256 .. 8192 tokens (32 + 8 heads of 128, 917 MB): 167.5 us, 84 % of
+// the copy rate, issue slots 56 % and the SM clock held down by the power limit; 8
+// of 32768 .. 131072 (855 MB): 152 us, 86 %.  Few short contexts are bound by the
+// chain of dependent reads (lengths, block ids, tiles, parts): one of 77 tokens
+// 7.2 us, 64 of 128 .. 2048 at D = 64 14.5 us.
 #include <float.h>
 #include <math.h>
 
@@ -702,7 +710,9 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
                                              : smem + S::ring_off + warp * S::kRing);
             store_row(part + row * D + g * (D / 8), y);
             if (g == 0) {
-              sh.ml[warp][slot][row][0] = m[n][c];
+              // (a part whose scores are all NaN has no maximum: it must not pass
+              // for an empty one)
+              sh.ml[warp][slot][row][0] = sum == sum ? m[n][c] : INFINITY;
               sh.ml[warp][slot][row][1] = sum;
             }
           }
@@ -719,6 +729,16 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
         pm.valid = 1;
       }
       if (pos < pos1) cu.next_unit(p);
+    }
+    if (!ok) {  // the stages from the one waited for on to the last one issued
+      const uint64_t t0 = globaltimer();
+      do {
+        drain_bar(bars + 8 * at, phase, t0);
+        if (++at == S::kStages) {
+          at = 0;
+          phase ^= 1;
+        }
+      } while (at != put);
     }
   }
   __syncthreads();

@@ -30,6 +30,7 @@ int rope_append_impl(void* q_out, const void* q, int64_t q_stride, const void* k
     return PA_ERR_INVALID;
   if (dtype != PA_DTYPE_F32 && dtype != PA_DTYPE_BF16) return PA_ERR_UNSUPPORTED;
   if (block_size != kBlockSize || !supported_dim(head_dim)) return PA_ERR_UNSUPPORTED;
+  if (num_q_heads + 2 * (int64_t)num_kv_heads > 1 << 30) return PA_ERR_UNSUPPORTED;  // 32-bit rows
   // a lane's two vectors are the two sides of eight rotation pairs; the 4-bit
   // groups pair neighbouring lanes
   if (rotary_dim % (fp4 && !interleaved ? 32 : 16) != 0) return PA_ERR_UNSUPPORTED;

@@ -86,6 +86,15 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   }
 }
 
+// What a role that gives up does before it returns, for its own copies and MMAs
+// still under way: waits for their phase whatever the abort flag says, until
+// limit_ns after t0.
+__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity, uint64_t t0,
+                                          unsigned long long limit_ns = kSpinLimitNs) {
+  while (!mbar_try_wait_sleep(bar, parity, kWaitSuspendNs))
+    if (globaltimer() - t0 > limit_ns) return;
+}
+
 // Spin until ready() holds.  Gives up (returns false) when another role of the
 // CTA has given up, or after limit_ns, in which case it records the timeout and
 // raises the abort flag.

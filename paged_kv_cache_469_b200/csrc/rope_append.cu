@@ -34,7 +34,7 @@ namespace {
 
 // Small CTAs: a warp is done after two round trips to memory, and its place is
 // free at once (8 warps: 46.8 us for 8192 tokens of 32 + 2 x 8 heads of 128 in
-// bf16, 205 MB; 4 warps: 41.7)
+// bf16, 205 MB; 4 warps: 41.7, both with one item per warp)
 constexpr int kWarps = 4;
 
 // eight consecutive elements
@@ -150,118 +150,119 @@ rope_append_kernel(const RopeAppendParams p, int chunks, int64_t items) {
   int64_t pos = p.rotary_dim > 0 ? p.positions[tok] : 0;
 #pragma unroll 1
   while (true) {
-  const int row0 = (int)(item - tok * chunks) * (kRows * U) + sub;
-  Raw8<T> a[U], b[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int r = min(row0 + u * kRows, n - 1);  // past the last row: that row again, unused
-    const T* src = r < nk   ? (const T*)p.q + tok * p.q_stride + (int64_t)r * D
-                   : r < nv ? (const T*)p.k + tok * p.k_stride + (int64_t)(r - nk) * D
-                            : (const T*)p.v + tok * p.v_stride + (int64_t)(r - nv) * D;
-    a[u].load(src + 8 * va);
-    b[u].load(src + 8 * vb);
-  }
-  const bool stored = slot >= 0 && slot < (int64_t)p.num_blocks * kBlockSize;
-  const int64_t blk = slot / kBlockSize;
-  const int off = (int)(slot % kBlockSize);
-  // without an angle the token is left out
-  const bool placed = p.rotary_dim == 0 || (pos >= 0 && pos < p.max_position);
-  float c[8], s[8];
-  if (placed && rotated && row0 < nv) {
-    const float* t = p.cos_sin + pos * p.rotary_dim + 8 * l;
-    load8(t, c);
-    load8(t + p.rotary_dim / 2, s);
-  }
-  // the next item's
-  const int64_t item2 = item + step, tok1 = tok;
-  if (item2 < items) {
-    tok = item2 / chunks;
-    slot = p.slot_mapping[tok];
-    pos = p.rotary_dim > 0 ? p.positions[tok] : 0;
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int r = row0 + u * kRows;
-    // every lane of the warp stays in the loop: the 4-bit groups' maxima are
-    // exchanged between lanes of a row
-    const bool live = placed && r < n && (r < nk || stored);
-    float x[8], y[8];
-    a[u].values(x);
-    b[u].values(y);
-    const bool turn = rotated && r < nv;
-    if (turn) {
-      if (p.interleaved) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float x0 = x[2 * j], x1 = x[2 * j + 1], y0 = y[2 * j], y1 = y[2 * j + 1];
-          x[2 * j] = __fsub_rn(__fmul_rn(x0, c[j]), __fmul_rn(x1, s[j]));
-          x[2 * j + 1] = __fadd_rn(__fmul_rn(x1, c[j]), __fmul_rn(x0, s[j]));
-          y[2 * j] = __fsub_rn(__fmul_rn(y0, c[4 + j]), __fmul_rn(y1, s[4 + j]));
-          y[2 * j + 1] = __fadd_rn(__fmul_rn(y1, c[4 + j]), __fmul_rn(y0, s[4 + j]));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x0 = x[j], y0 = y[j];
-          x[j] = __fsub_rn(__fmul_rn(x0, c[j]), __fmul_rn(y0, s[j]));
-          y[j] = __fadd_rn(__fmul_rn(y0, c[j]), __fmul_rn(x0, s[j]));
-        }
-      }
+    const int row0 = (int)(item - tok * chunks) * (kRows * U) + sub;
+    Raw8<T> a[U], b[U];
+  #pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = min(row0 + u * kRows, n - 1);  // past the last row: that row again, unused
+      const T* src = r < nk   ? (const T*)p.q + tok * p.q_stride + (int64_t)r * D
+                     : r < nv ? (const T*)p.k + tok * p.k_stride + (int64_t)(r - nk) * D
+                              : (const T*)p.v + tok * p.v_stride + (int64_t)(r - nv) * D;
+      a[u].load(src + 8 * va);
+      b[u].load(src + 8 * vb);
     }
-    if constexpr (kFp4) {
-      const bool is_v = r >= nv;
-      const int h = r - (is_v ? nv : nk);
-      const float g = is_v ? p.v_scale : p.k_scale, six_g = is_v ? p.v_six : p.k_six;
-      // interleaved: a lane holds a whole group; else each half of a group
-      // lies with the neighbouring lane
-      if (row0 - sub + u * kRows + kRows > nk) {  // (of the warp's rows, not this lane's)
-      float ma = absmax8(x), mb = absmax8(y);
-      const float oa = __shfl_xor_sync(0xffffffffu, ma, 1);
-      const float ob = __shfl_xor_sync(0xffffffffu, mb, 1);
-      if (p.interleaved) {
-        ma = mb = max_nan(ma, mb);
-      } else {
-        ma = max_nan(ma, oa);
-        mb = max_nan(mb, ob);
-      }
-      if (live && r >= nk) {
-        uint8_t* tile = (uint8_t*)p.k_cache + (blk * p.num_kv_heads + h) * (int64_t)Tile::bytes;
-        const uint32_t sa = group_scale(ma, six_g), sb = group_scale(mb, six_g);
-        const uint32_t wa = codes8(x, sa, g), wb = codes8(y, sb, g);
-        if (is_v) {
-          *(uint32_t*)(tile + Tile::v_word(off, va)) = wa;
-          *(uint32_t*)(tile + Tile::v_word(off, vb)) = wb;
-          if (va % 2 == 0) tile[Tile::v_scale(off, va / 2)] = (uint8_t)sa;
-          if (vb % 2 == 0) tile[Tile::v_scale(off, vb / 2)] = (uint8_t)sb;
+    const bool stored = slot >= 0 && slot < (int64_t)p.num_blocks * kBlockSize;
+    const int64_t blk = slot / kBlockSize;
+    const int off = (int)(slot % kBlockSize);
+    // without an angle the token is left out
+    const bool placed = p.rotary_dim == 0 || (pos >= 0 && pos < p.max_position);
+    float c[8], s[8];
+    if (placed && rotated && row0 < nv) {
+      const float* t = p.cos_sin + pos * p.rotary_dim + 8 * l;
+      load8(t, c);
+      load8(t + p.rotary_dim / 2, s);
+    }
+    // the next item's
+    const int64_t item2 = item + step, tok1 = tok;
+    if (item2 < items) {
+      tok = item2 / chunks;
+      slot = p.slot_mapping[tok];
+      pos = p.rotary_dim > 0 ? p.positions[tok] : 0;
+    }
+  #pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = row0 + u * kRows;
+      // every lane of the warp stays in the loop: the 4-bit groups' maxima are
+      // exchanged between lanes of a row
+      const bool live = placed && r < n && (r < nk || stored);
+      float x[8], y[8];
+      a[u].values(x);
+      b[u].values(y);
+      const bool turn = rotated && r < nv;
+      if (turn) {
+        if (p.interleaved) {
+  #pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x0 = x[2 * j], x1 = x[2 * j + 1], y0 = y[2 * j], y1 = y[2 * j + 1];
+            x[2 * j] = __fsub_rn(__fmul_rn(x0, c[j]), __fmul_rn(x1, s[j]));
+            x[2 * j + 1] = __fadd_rn(__fmul_rn(x1, c[j]), __fmul_rn(x0, s[j]));
+            y[2 * j] = __fsub_rn(__fmul_rn(y0, c[4 + j]), __fmul_rn(y1, s[4 + j]));
+            y[2 * j + 1] = __fadd_rn(__fmul_rn(y1, c[4 + j]), __fmul_rn(y0, s[4 + j]));
+          }
         } else {
-          *(uint32_t*)(tile + Tile::k_word(off, va)) = wa;
-          *(uint32_t*)(tile + Tile::k_word(off, vb)) = wb;
-          if (va % 2 == 0) tile[Tile::k_scale(off, va / 2)] = (uint8_t)sa;
-          if (vb % 2 == 0) tile[Tile::k_scale(off, vb / 2)] = (uint8_t)sb;
+  #pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float x0 = x[j], y0 = y[j];
+            x[j] = __fsub_rn(__fmul_rn(x0, c[j]), __fmul_rn(y0, s[j]));
+            y[j] = __fadd_rn(__fmul_rn(y0, c[j]), __fmul_rn(x0, s[j]));
+          }
         }
-        continue;
       }
+      if constexpr (kFp4) {
+        const bool is_v = r >= nv;
+        const int h = r - (is_v ? nv : nk);
+        const float g = is_v ? p.v_scale : p.k_scale, six_g = is_v ? p.v_six : p.k_six;
+        // interleaved: a lane holds a whole group; else each half of a group
+        // lies with the neighbouring lane
+        // (asked of the warp's rows, not of this lane's)
+        if (row0 - sub + u * kRows + kRows > nk) {
+          float ma = absmax8(x), mb = absmax8(y);
+          const float oa = __shfl_xor_sync(0xffffffffu, ma, 1);
+          const float ob = __shfl_xor_sync(0xffffffffu, mb, 1);
+          if (p.interleaved) {
+            ma = mb = max_nan(ma, mb);
+          } else {
+            ma = max_nan(ma, oa);
+            mb = max_nan(mb, ob);
+          }
+          if (live && r >= nk) {
+            uint8_t* tile = (uint8_t*)p.k_cache + (blk * p.num_kv_heads + h) * (int64_t)Tile::bytes;
+            const uint32_t sa = group_scale(ma, six_g), sb = group_scale(mb, six_g);
+            const uint32_t wa = codes8(x, sa, g), wb = codes8(y, sb, g);
+            if (is_v) {
+              *(uint32_t*)(tile + Tile::v_word(off, va)) = wa;
+              *(uint32_t*)(tile + Tile::v_word(off, vb)) = wb;
+              if (va % 2 == 0) tile[Tile::v_scale(off, va / 2)] = (uint8_t)sa;
+              if (vb % 2 == 0) tile[Tile::v_scale(off, vb / 2)] = (uint8_t)sb;
+            } else {
+              *(uint32_t*)(tile + Tile::k_word(off, va)) = wa;
+              *(uint32_t*)(tile + Tile::k_word(off, vb)) = wb;
+              if (va % 2 == 0) tile[Tile::k_scale(off, va / 2)] = (uint8_t)sa;
+              if (vb % 2 == 0) tile[Tile::k_scale(off, vb / 2)] = (uint8_t)sb;
+            }
+            continue;
+          }
+        }
+      }
+      if (!live) continue;
+      T* dst;
+      if (r < nk) {
+        dst = (T*)p.q_out + (tok1 * nk + r) * (int64_t)D;
+      } else {
+        const int h = r - (r < nv ? nk : nv);
+        dst = (T*)(r < nv ? p.k_cache : p.v_cache) +
+              ((blk * p.num_kv_heads + h) * kBlockSize + off) * (int64_t)D;
+      }
+      if (turn) {
+        store8(dst + 8 * va, x);
+        store8(dst + 8 * vb, y);
+      } else {  // bit-exact copy
+        a[u].store(dst + 8 * va);
+        b[u].store(dst + 8 * vb);
       }
     }
-    if (!live) continue;
-    T* dst;
-    if (r < nk) {
-      dst = (T*)p.q_out + (tok1 * nk + r) * (int64_t)D;
-    } else {
-      const int h = r - (r < nv ? nk : nv);
-      dst = (T*)(r < nv ? p.k_cache : p.v_cache) +
-            ((blk * p.num_kv_heads + h) * kBlockSize + off) * (int64_t)D;
-    }
-    if (turn) {
-      store8(dst + 8 * va, x);
-      store8(dst + 8 * vb, y);
-    } else {  // bit-exact copy
-      a[u].store(dst + 8 * va);
-      b[u].store(dst + 8 * vb);
-    }
-  }
-  if (item2 >= items) break;
-  item = item2;
+    if (item2 >= items) break;
+    item = item2;
   }
 }
 
@@ -340,7 +341,7 @@ cudaError_t launch_rope(const RopeAppendParams& p, cudaStream_t stream) {
   constexpr int kRows = 32 / (D / 16);
   // row sets per warp once every SM has its fill of warps: more loads in
   // flight against more registers (8192 bf16 tokens as above: 43.1 us with two,
-  // 41.7 with three or four; quantising, 4099 tokens: 27.8, 33.1, 33.8)
+  // 41.7 with three or four, one item per warp; quantising, 4099 tokens: 27.8, 33.1, 33.8)
   constexpr int kWide = kFp4 ? 2 : 3;
   static std::atomic<int> known1[64], known[64];
   const int n = p.num_q_heads + 2 * p.num_kv_heads;
@@ -348,8 +349,9 @@ cudaError_t launch_rope(const RopeAppendParams& p, cudaStream_t stream) {
   auto go = [&](auto kernel, int u, std::atomic<int> (&known)[64]) {
     const int chunks = (n + kRows * u - 1) / (kRows * u);
     const int64_t items = (int64_t)p.num_tokens * chunks;
-    // one wave of CTAs exactly (8192 bf16 tokens as above: 37.7 us; with one
-    // more per SM than fits 48.0, one less 41.4)
+    // one wave of CTAs exactly (8192 bf16 tokens as above: 37.2 us, 84 % of the
+    // copy rate; with one
+    // more per SM than fits 48.0, with one less 41.4)
     const int64_t grid =
         min((items + kWarps - 1) / kWarps,
             (int64_t)device_sm_count() * resident_ctas(kernel, kWarps * 32, known));

@@ -237,6 +237,38 @@ def test_a_nan_query_stays_in_its_row():
         assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], want[~bad])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,qls", [([4000, 70], [1, 1]), ([1300, 900], [9, 1]),
+                                      ([1500] * 9, [300] + [512] * 8)])
+def test_a_nan_in_the_cache_reaches_the_rows_that_see_it(lens, qls, dtype):
+    """Also where a whole part of a sequence's keys holds nothing else; the rows that
+    do not see it, the other heads' and the other sequences' stay as they were."""
+    hq, hkv, d = 8, 2, 128
+    st = Step(sum(lens), lens, qls, hq, hkv, d, dtype)
+    want, pool = st.run(), st.pool.copy()
+    first, last = lens[0] - qls[0] // 2 - 500, lens[0] - qls[0] // 2
+    sees = torch.arange(st.qsl[-1]) >= qls[0] + first - lens[0]
+    sees[qls[0]:] = False
+    for tok in range(first, last):  # K of head 1
+        tile = pool[st.tables[0, tok // 16], 1]
+        tile[16 * d + tok % 16 * (d // 16):][:d // 16] = 127
+    st.cache.copy_(torch.from_numpy(pool))
+    got = st.run()
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[sees, 4:] = True
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], want[~bad])
+
+    pool = st.pool.copy()
+    for tok in range(first, last):  # V of head 0, dims 32 .. 47
+        pool[st.tables[0, tok // 16], 0, 17 * d + 2 * 16 + tok % 16] = 127
+    st.cache.copy_(torch.from_numpy(pool))
+    got = st.run()
+    assert torch.isnan(got[sees, :4, 32:48]).all()
+    kept = torch.ones_like(got, dtype=torch.bool)
+    kept[:qls[0], :4, 32:48] = False
+    assert torch.equal(got[kept], want[kept])
+
+
 def test_a_prefix_shared_by_sequences_and_repeated_blocks():
     st = Step(13, [400, 400, 64], [1, 90, 1], 8, 2, 128, junk=False)
     st.tables[1, :10] = st.tables[0, :10]
