@@ -292,6 +292,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint32_t sh_tmem_base;
   __shared__ int sh_abort;
+  __shared__ int sh_loaded;  // the last item whose Q was asked for
   __shared__ int sh_item[kItemRing];
 
   // (from one lane: the compiler then keeps what follows from it, above all the
@@ -306,6 +307,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
 
   if (threadIdx.x == 0) {
     sh_abort = 0;
+    sh_loaded = -1;
     mbar_init(bar(kBarQFull), 1);
     mbar_init(bar(kBarQReady), 8);  // one arrival per softmax warp
     mbar_init(bar(kBarQEmpty), 1);
@@ -382,7 +384,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       for (int i = 0; i < 2; ++i) sh[i].load_k(tile_of(ids_n, k0 + kProducers * i, nxt.kvh), lane);
       uint32_t g = 0;  // global tile counter
       bool ok = true;
-      int item = -1, loaded = -1;  // (the last one whose Q is on its way)
+      int item = -1;
       while (!nxt.done && ok) {
         cur = nxt;
         const int ids = ids_n;
@@ -394,7 +396,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
             if (ok) {
               const ItemInfo it = load_item(p, work, cur.w);
               mbar_expect_tx(bar(kBarQFull), 2 * LY::kBytes);
-              loaded = item;
+              sh_loaded = item;
               for (int h = 0; h < 2; ++h) {
                 const int head = pair_heads ? it.head0 + h : it.head0;
                 const int qt = pair_heads ? it.qt0 : it.qt0 + h;
@@ -455,8 +457,6 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         __syncwarp();
         ++g;
       }
-      if (!ok && warp == kWarpQ && lane == 0 && loaded >= 0)
-        drain_bar(bar(kBarQFull), loaded & 1, globaltimer());
     } else if (warp == kWarpMma) {
       // =========================== MMA issuer ===========================
       // (as in the bf16 kernel: P.V of tile g-1 before Q K^T of tile g, per half)
@@ -728,6 +728,8 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
   // ---- wind down: every role is done (or gave up); free TMEM
   tc_fence_before();
   __syncthreads();
+  if (sh_abort && threadIdx.x == 0 && sh_loaded >= 0)
+    drain_bar(bar(kBarQFull), sh_loaded & 1, globaltimer());
   if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
