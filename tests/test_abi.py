@@ -197,6 +197,7 @@ def test_rope_append_argument_checks(L, fp4):
     assert c(bs=32) == palib.PA_ERR_UNSUPPORTED
     assert c(dt=2) == palib.PA_ERR_UNSUPPORTED
     assert c(r=40) == palib.PA_ERR_UNSUPPORTED
+    assert c(hq=(1 << 31) - 1) == c(hkv=1 << 30) == palib.PA_ERR_UNSUPPORTED  # rows past 32 bits
     assert c(r=80) == palib.PA_ERR_INVALID          # more than head_dim
     assert c(r=-16) == palib.PA_ERR_INVALID
     assert c(T=-1) == palib.PA_ERR_INVALID
