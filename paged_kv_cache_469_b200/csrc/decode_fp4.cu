@@ -104,6 +104,12 @@ struct Shape {
   // contexts of 128 .. 2048 at D = 64, 8 rows: 14.7 us, with half of it 17.0; 33
   // of 40 .. 3000 with 13 drafted tokens, 16 rows: 18.7, with half of it 21.2.
   static constexpr int kWhole = R * kWarps;
+  // Parts of a unit that one CTA joins at once; of more, groups of so many first.
+  // Two steps cost 2 to 4 us more than one of as many parts as that: four
+  // contexts of 7236 .. 28944 at D = 64, 30 parts, 16.0 us, 21.1 in two steps.
+  static constexpr int kJoin = 32, kGroup = 12;
+  static_assert(kFp4MaxCtas <= 32 * kGroup && kJoin <= 32, "a lane per part");
+  static_assert(kRing * kWarps >= R * 33 * 4, "the weights of a join");
   static_assert(kStages >= 3 && kRing >= kPart, "a warp's last part takes its ring's place");
 };
 
@@ -126,6 +132,12 @@ struct Run {
   int before, complete;  // starts in an earlier CTA; starts and ends here
 };
 
+// A join under way: the CTA of its first part, CTAs from one part to the next, and
+// their number; whether the unit starts with it, and is whole after it
+struct Join {
+  int first, apart, n, starts, whole;
+};
+
 template <typename S>
 struct Shared {
   unsigned long long bars[S::kWarps * S::kStages];
@@ -137,7 +149,8 @@ struct Shared {
   Run runs[S::kWarps + 1];
   int cut[2];  // this CTA's stretch
   int abort;
-  int last[2];
+  Join join[2];
+  int last[2];  // this CTA arrived last at its first, its last unit
 };
 
 template <int R>
@@ -710,9 +723,7 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
                                              : smem + S::ring_off + warp * S::kRing);
             store_row(part + row * D + g * (D / 8), y);
             if (g == 0) {
-              // (a part whose scores are all NaN has no maximum: it must not pass
-              // for an empty one)
-              sh.ml[warp][slot][row][0] = sum == sum ? m[n][c] : INFINITY;
+              sh.ml[warp][slot][row][0] = m[n][c];
               sh.ml[warp][slot][row][1] = sum;
             }
           }
@@ -775,6 +786,8 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
     // the run is loaded and dropped)
     float* start = sh.ml[w0][1][row];
     float m[W + 1], sum = 0.f;
+    // (a part whose scores are all NaN has no maximum and no weight, but its O is
+    // NaN, and so is the sum with it)
     m[W] = before ? -INFINITY : start[0];
     float mx = m[W];
 #pragma unroll
@@ -807,18 +820,32 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
     if (row >= pm.nrows) continue;
     const unsigned mine = run.mine;
     float y[4] = {0.f, 0.f, 0.f, 0.f};
-    auto add = [&](const unsigned char* part, float f) {
-      const float4 v = *(const float4*)((const float*)part + off);
+    auto add = [&](float f, const float4& v) {
       y[0] = fmaf(f, v.x, y[0]);
       y[1] = fmaf(f, v.y, y[1]);
       y[2] = fmaf(f, v.z, y[2]);
       y[3] = fmaf(f, v.w, y[3]);
     };
-    if (!run.before) add(smem + S::ring_off + run.w0 * S::kRing, sh.ml[run.w0][1][row][0]);
-#pragma unroll 2
-    for (unsigned left = mine; left; left &= left - 1) {
-      const int w = __ffs(left) - 1;
-      add(smem + S::part_off + w * S::kPart, sh.ml[w][0][row][0]);
+    if (!run.before)
+      add(sh.ml[run.w0][1][row][0],
+          *(const float4*)((const float*)(smem + S::ring_off + run.w0 * S::kRing) + off));
+#pragma unroll 1
+    for (unsigned left = mine; left;) {  // four parts' loads together
+      float4 v[4];
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int w = __ffs(left) - 1;
+        left &= left - 1;
+        f[e] = 0.f;
+        v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w >= 0) {
+          f[e] = sh.ml[w][0][row][0];
+          v[e] = *(const float4*)((const float*)(smem + S::part_off + w * S::kPart) + off);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) add(f[e], v[e]);
     }
     if (run.complete) {
       const float f = sh.ml[run.w0][1][row][1];
@@ -840,64 +867,128 @@ __global__ void __launch_bounds__(S::kWarps * 32, 1) decode_fp4_kernel(const Fp4
   if (!pending[0] && !pending[1]) return;
 
   // ---- a unit in several CTAs: the one that arrives last joins its parts, in
-  // the order of the CTAs
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    int mine = 0;
-    if (threadIdx.x == 0 ? pending[0] : pending[1]) {
-      const PartMeta& f = threadIdx.x == 0 ? sh.meta[sh.runs[0].w0][0] : sh.meta[tail.w0][1];
-      const int c0 = divide(f.unit_start, per), c1 = divide(f.unit_start + f.nblk - 1, per);
-      mine = atomicAdd(p.ws_counters + c0, 1) == c1 - c0;
-      if (mine) p.ws_counters[c0] = 0;  // every part has arrived: zero for the next call
-    }
-    sh.last[threadIdx.x] = mine;
-  }
-  __syncthreads();
+  // the order of the CTAs; of many parts, the last of each group of CTAs joins the
+  // group's first, in the place of its first part.  (Two contexts of 8270 and 33083
+  // on one kv-head, fp32, 148 parts: 16.8 us, 34.6 when one warp per row took them all.)
+  unsigned open = (pending[0] ? 1u : 0u) | (pending[1] ? 2u : 0u);
+  float* weight = (float*)(smem + S::ring_off);  // [row][part], of the join under way
+  float* total = weight + R * 32;                // [row]: their maximum, and sum
 #pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
-    if (!sh.last[side]) continue;
-    __threadfence();
-    const PartMeta& f = side == 0 ? sh.meta[sh.runs[0].w0][0] : sh.meta[tail.w0][1];
-    const int c0 = divide(f.unit_start, per), c1 = divide(f.unit_start + f.nblk - 1, per);
-    for (int row = warp; row < f.nrows; row += W) {
-      auto slot = [&](int c) { return (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * 16 + row; };
-      float y[D / 32], sum = 0.f, mx = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) y[i] = 0.f;
-      for (int cc = c0; cc <= c1; cc += 32) {  // a lane's weight each, then the parts
-        const int c = cc + lane;
-        const float2 ml = c <= c1 ? __ldcg((const float2*)(p.ws_ml + slot(c) * 2))
-                                  : make_float2(-INFINITY, 0.f);
-        float top = ml.x;
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-        if (top > mx) {
-          const float old = ex2(mx - top);
-          mx = top;
-          sum *= old;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) y[i] *= old;
+  for (int level = 0; level < 2; ++level) {
+    __syncthreads();
+    if (threadIdx.x < 2) {
+      int mine = 0;
+      if (open >> threadIdx.x & 1) {
+        // the unit's CTAs, and the parts that are joined at this level
+        const PartMeta& f = threadIdx.x == 0 ? sh.meta[sh.runs[0].w0][0] : sh.meta[tail.w0][1];
+        const int c0 = divide(f.unit_start, per);
+        const int all = divide(f.unit_start + f.nblk - 1, per) - c0 + 1;
+        const bool grouped = all > S::kJoin, whole = !grouped || level == 1;
+        int first = c0, n = all;
+        if (grouped) {
+          n = (all + S::kGroup - 1) / S::kGroup;
+          if (level == 0) {
+            first += ((int)blockIdx.x - c0) / S::kGroup * S::kGroup;
+            n = min(S::kGroup, c0 + all - first);
+          }
         }
-        const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
-        sum = fmaf(wt, ml.y, sum);
-        const int n = min(c1 - cc + 1, 32);
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-          const float f1 = __shfl_sync(0xffffffffu, wt, i);
-          const float* part = p.ws_o + slot(cc + i) * D + lane * (D / 32);
+        int* counter = p.ws_counters + (whole ? c0 : kFp4MaxCtas + 2 * first + (first == c0));
+        __threadfence();  // this CTA's parts, before its arrival
+        mine = atomicAdd(counter, 1) == n - 1;
+        __threadfence();  // and the others' after theirs
+        if (mine) *counter = 0;  // every part has arrived: zero for the next call
+        sh.join[threadIdx.x] = Join{first, grouped && whole ? S::kGroup : 1, n, first == c0, whole};
+      }
+      sh.last[threadIdx.x] = mine;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+      if (!sh.last[side]) open &= ~(1u << side);
+      if (!(open >> side & 1)) continue;
+      const PartMeta& f = side == 0 ? sh.meta[sh.runs[0].w0][0] : sh.meta[tail.w0][1];
+      const Join join = sh.join[side];
+      const int n = join.n;
+      const bool whole = join.whole;
+      // rows of part i in the workspace (a unit's first part is its CTA's last)
+      auto slot = [&](int i) {
+        return ((join.first + i * join.apart) * 2 + (i == 0 && join.starts)) * 16;
+      };
+      // four dims of a row per thread; the first parts' loads leave while the
+      // weights are made
+      int i = threadIdx.x;
+      const int quads = f.nrows * kQuads;
+      constexpr int kBatch = 12;
+      float4 v[kBatch];
+      auto load = [&](int k) {
+        const float4* src = (const float4*)p.ws_o + i;
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k) y[k] = fmaf(f1, __ldcg(part + k), y[k]);
+        for (int e = 0; e < kBatch; ++e) v[e] = __ldcg(src + slot(min(k + e, n - 1)) * kQuads);
+      };
+      if (i < quads) load(0);
+      constexpr int kTimes = (R + W - 1) / W;  // rows of a warp; a lane per part (at most 32)
+      float2 mls[kTimes];
+#pragma unroll
+      for (int e = 0; e < kTimes; ++e)
+        mls[e] = lane < n && warp + e * W < f.nrows
+                     ? __ldcg((const float2*)(p.ws_ml + (slot(lane) + warp + e * W) * 2))
+                     : make_float2(-INFINITY, 0.f);
+      __syncthreads();  // the join before has read its weights
+#pragma unroll
+      for (int e = 0; e < kTimes; ++e) {
+        const int row = warp + e * W;
+        if (row >= f.nrows) break;
+        const float2 ml = mls[e];
+        float mx = ml.x;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+        const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
+        float sum = wt == 0.f ? 0.f : wt * ml.y;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        weight[row * 32 + lane] = wt;
+        if (lane == 0) {
+          total[row] = whole ? p.v_scale / sum : 1.f;
+          if (!whole) *(float2*)(p.ws_ml + (slot(0) + row) * 2) = make_float2(mx, sum);
         }
       }
+      __syncthreads();
+#pragma unroll 1
+      while (i < quads) {
+        const int row = i / kQuads, off = row * D + i % kQuads * 4;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int k = 0;;) {
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-      const int rr = f.row0 + row, j = token_of(p, rr);
-      T* dst = (T*)p.out + ((int64_t)(f.q0 + j) * p.num_q_heads + f.head * p.group +
-                            (rr - j * p.group)) * D + lane * (D / 32);
+          for (int e = 0; e < kBatch; ++e) {
+            if (k + e >= n) break;
+            const float w = weight[row * 32 + k + e];
+            y[0] = fmaf(w, v[e].x, y[0]);
+            y[1] = fmaf(w, v[e].y, y[1]);
+            y[2] = fmaf(w, v[e].z, y[2]);
+            y[3] = fmaf(w, v[e].w, y[3]);
+          }
+          k += kBatch;
+          if (k >= n) break;
+          load(k);
+        }
+        if (whole) {
+          const float s = total[row];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) dst[i] = (T)(y[i] * (p.v_scale / sum));
+          for (int k = 0; k < 4; ++k) y[k] *= s;
+          const int rr = f.row0 + row, j = token_of(p, rr);
+          store_dims<T>((T*)p.out + ((int64_t)(f.q0 + j) * p.num_q_heads + f.head * p.group +
+                                     (rr - j * p.group)) * D + i % kQuads * 4,
+                        y);
+        } else {  // (only this thread reads these elements of the parts)
+          *(float4*)(p.ws_o + slot(0) * D + off) = make_float4(y[0], y[1], y[2], y[3]);
+        }
+        i += W * 32;
+        if (i < quads) load(0);
+      }
+      if (whole) open &= ~(1u << side);
     }
+    if (!open) return;
   }
 }
 

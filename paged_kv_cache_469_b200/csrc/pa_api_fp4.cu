@@ -91,7 +91,7 @@ int rope_append_impl(void* q_out, const void* q, int64_t q_stride, const void* k
 }
 
 // Workspace of attention over a 4-bit cache: the 256-byte header, the arrival
-// counters, two partial results per CTA, and the prefill work list.
+// counters (of a CTA's unit, and two of groups of CTAs), two partial results per CTA, and the prefill work list.
 struct Fp4Workspace {
   int max_items;
   size_t counters_off, ml_off, o_off, items_off, total;
@@ -99,7 +99,7 @@ struct Fp4Workspace {
 Fp4Workspace fp4_workspace(int num_seqs, int num_tokens, int num_q_heads, int head_dim) {
   Fp4Workspace w{};
   w.counters_off = 256;
-  w.ml_off = w.counters_off + kFp4MaxCtas * sizeof(int);
+  w.ml_off = w.counters_off + kFp4MaxCtas * 3 * sizeof(int);
   w.o_off = w.ml_off + (size_t)kFp4MaxCtas * 2 * 16 * 2 * sizeof(float);
   w.items_off = w.o_off + (size_t)kFp4MaxCtas * 2 * 16 * head_dim * sizeof(float);
   // a sequence's query tiles times the heads at most, one item each

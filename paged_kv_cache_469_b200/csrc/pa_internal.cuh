@@ -213,7 +213,8 @@ struct Fp4AttnParams {
   float v_scale;
   int max_q;         // decode kernel: sequences with more query tokens are not its own
   int* ws_status;    // the workspace header
-  int* ws_counters;  // [kFp4MaxCtas]: arrivals at a unit that starts in that CTA, zero between calls
+  int* ws_counters;  // [3][kFp4MaxCtas]: arrivals at a unit that starts in that CTA, and at
+                     // groups of parts that start there (two to a CTA); zero between calls
   float* ws_ml;      // [kFp4MaxCtas][2][16][2] running max (log2 units) and sum
   float* ws_o;       // [kFp4MaxCtas][2][16][D] unnormalised partial outputs
 };

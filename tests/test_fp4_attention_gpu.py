@@ -169,6 +169,22 @@ def test_long_contexts_over_many_processors(hq, hkv, d, lens):
         assert torch.equal(a, st.run())
 
 
+@pytest.mark.parametrize("hq,hkv,d,lens,qls", [
+    (16, 1, 128, [8727] * 5, [1] * 5),                # 30 processors a unit
+    (8, 1, 64, [8270, 33083], [1, 1]),                # 30 and 118
+    (16, 1, 64, [9000, 21000, 5], [4, 2, 1]),         # several units of one sequence
+    (8, 1, 128, [40000], [1]),                        # all of them
+    (7, 1, 64, [7300, 6900], [3, 3]),                 # about the size joined at once
+])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_units_over_many_processors(hq, hkv, d, lens, qls, dtype):
+    st = Step(sum(lens) + d, lens, qls, hq, hkv, d, dtype)
+    a = st.run()
+    st.check(a)
+    assert torch.equal(a, st.run(host=True)) and torch.equal(a, st.run())
+    st.check(a)
+
+
 @pytest.mark.parametrize("lens,qls", [([300, 45, 517], [1, 200, 2]),  # (45: left out, its rows stay)
                                       ([300, 245, 517], [1, 200, 2]),
                                       ([400] * 24, [250] * 24)])  # (on the tensor cores)
