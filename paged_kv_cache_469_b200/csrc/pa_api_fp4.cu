@@ -124,6 +124,7 @@ Fp4Costs fp4_costs(int head_dim) {
   return head_dim == 128 ? Fp4Costs{{60., 93.}, 1950., 24, 44} : Fp4Costs{{38., 50.}, 1800., 36, 72};
 }
 constexpr double kLaunchNs = 8000.;  // a kernel's start and end
+constexpr double kJoinNs = 4000.;    // and the join of an item's parts
 
 // The prefill kernel's work of a step.
 struct PrefillLoad {
@@ -131,6 +132,8 @@ struct PrefillLoad {
   // its time on n SMs: the items are given out heaviest first
   double ns(int n, double tile_ns) const {
     if (items <= 0.) return 0.;
+    const int ctas = prefill_fp4_cluster(items, longest, n);  // of an item
+    if (ctas > 1) return tile_ns * ceil(longest / ctas) + kLaunchNs + kJoinNs;
     return tile_ns * (items <= n ? longest : max(longest, tiles / n + longest / 2)) + kLaunchNs;
   }
 };

@@ -261,6 +261,11 @@ cudaError_t launch_prefill_tcgen05(const AttnParams& p, int head_dim, int max_qu
                                    const int32_t* query_start_loc_host, cudaStream_t stream,
                                    int max_ctas);
 
+// CTAs of a cluster that shares an item of launch_prefill_fp4 on `sms` SMs, for that
+// many items of at most that many 128-key tiles: as many as leave every item a
+// cluster at once and every CTA two tiles.
+int prefill_fp4_cluster(double items, double tiles, int sms);
+
 // The same over a 4-bit cache (p.k_cache): p.scale_log2 holds its k_scale.
 cudaError_t launch_prefill_fp4(const AttnParams& p, float v_scale, int head_dim,
                                int max_query_len, const int32_t* seq_lens_host,

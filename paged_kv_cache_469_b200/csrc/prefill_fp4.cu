@@ -32,6 +32,12 @@
 // the one before has two tiles left: the list is heaviest first, so the CTAs
 // end close together.
 //
+// Fewer items than half the SMs are cut along their keys: a cluster of two to eight
+// CTAs takes an item, each an equal stretch of its tiles, and each joins an equal
+// share of its rows from the others' shared memory.  One chunk of 512 over 8192
+// tokens, 64 items: 89 us, 133 without; two of 247 over up to 2953 on one kv-head,
+// 32 items: 27.8, 53.7 without.
+//
 // Every mbarrier wait is bounded by a time limit; a wait that runs out sets a
 // status bit in the workspace and the CTA winds down instead of hanging.
 #include <cuda.h>
@@ -69,6 +75,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0, kTmemS = 256;    // + 128 * half
 constexpr float kRescaleThreshold = 8.0f;       // log2 units: move the max only past 2^8
 constexpr float kPShift = 7.0f;                 // P is held times 2^7
+constexpr int kMaxCluster = 8;                  // CTAs that share an item
 constexpr int kMaxChains = 8;                   // independent max chains over a row of scores
 
 template <int D>
@@ -84,7 +91,20 @@ struct Layout {
   // one CTA per SM (its tensor memory is all of the SM's)
   static constexpr int total = (used < 120 * 1024 ? 120 * 1024 : used) + 1024;
   static_assert(total <= 227 * 1024, "shared memory of one CTA");
+  static_assert(bar_off - k_off >= 2 * 128 * (4 * D + 8), "a part in the place of K and V");
 };
+
+// Where a part's row r lies in the stages of K and V once they are read: O in fp32,
+// its 16-byte units xor the row (the lanes of a store are 32 rows), and behind all
+// rows each one's maximum and sum.
+template <int D>
+__device__ __forceinline__ uint32_t part_at(uint32_t at, int r, int unit) {
+  return at + r * (4 * D) + ((unit ^ (r & (D / 4 - 1))) << 4);
+}
+template <int D>
+__device__ __forceinline__ uint32_t part_ml(uint32_t at, int r) {
+  return at + 2 * 128 * 4 * D + r * 8;
+}
 
 // mbarrier indices
 enum : int {
@@ -246,9 +266,43 @@ struct Share {
   }
 };
 
+// A cluster of several CTAs shares an item: each takes an equal stretch of its
+// tiles, and joins an equal share of its rows.
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ int cluster_ctas() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return (int)n;
+}
+// every thread of the cluster, its shared-memory writes before the others' reads
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// this CTA's shared-memory address in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// the tiles of an item that this CTA takes: all of them, but in a cluster
+template <bool kSplit>
+__device__ __forceinline__ int first_tile(int ntiles) {
+  return kSplit ? cluster_rank() * ntiles / cluster_ctas() : 0;
+}
+template <bool kSplit>
+__device__ __forceinline__ int end_tile(int ntiles) {
+  return kSplit ? (cluster_rank() + 1) * ntiles / cluster_ctas() : ntiles;
+}
+
 // The tiles of a CTA's items one after the other, as the producers walk them
+template <bool kSplit>
 struct TileCursor {
-  int k = -1, t = 0, ntiles = 0;  // item of this CTA, tile in it
+  int k = -1, t = 0, ntiles = 0;  // item of this CTA, tile in it, end of its tiles
   int w;                          // its place in the list
   int kvh, L, nblk;
   const int32_t* table;
@@ -265,8 +319,8 @@ struct TileCursor {
         return;
       }
       const ItemInfo it = load_item(p, work, w);
-      t = -1;
-      ntiles = it.ntiles;
+      t = first_tile<kSplit>(it.ntiles) - 1;
+      ntiles = end_tile<kSplit>(it.ntiles);
       kvh = it.head0 / p.group;
       L = it.L;
       nblk = (it.L + kBlockSize - 1) / kBlockSize;
@@ -283,7 +337,7 @@ struct TileCursor {
   }
 };
 
-template <int D>
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constant__ CUtensorMap tm_q,
                    int pair_heads, const __grid_constant__ PrefillWork work) {
@@ -366,11 +420,14 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         sh_item[k % kItemRing] = w;
         mbar_arrive(bar(kBarItem + k % kItemRing));
         // the last CTA to run out of items leaves the counters at zero
-        if (w >= num_items && atomicAdd(p.ws_header + kWsDone, 1) == (int)gridDim.x - 1)
+        if (!kSplit && w >= num_items && atomicAdd(p.ws_header + kWsDone, 1) == (int)gridDim.x - 1)
           p.ws_header[kWsClaim] = p.ws_header[kWsDone] = 0;
       };
-      if (warp == kWarpQ && lane == 0) publish(0, blockIdx.x);
-      TileCursor cur, nxt;
+      if (warp == kWarpQ && lane == 0) {
+        publish(0, kSplit ? blockIdx.x / cluster_ctas() : blockIdx.x);
+        if (kSplit) publish(1, INT32_MAX);  // one item to a cluster
+      }
+      TileCursor<kSplit> cur, nxt;
       nxt.next(p, work, num_items, item_at);
       int ids_n = nxt.ids(p, lane);
       auto tile_of = [&](int ids, int b, int kvh) -> const uint8_t* {
@@ -411,7 +468,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         }
         // the item after this one, when two of its tiles are left; made known at
         // the end of the first of them, when the counter has answered
-        const bool take = warp == kWarpQ && lane == 0 && cur.t == max(cur.ntiles - 2, 0);
+        const bool take = !kSplit && warp == kWarpQ && lane == 0 && cur.t == max(cur.ntiles - 2, 0);
         int taken = 0;
         if (take) {
           taken = (int)gridDim.x + atomicAdd(p.ws_header + kWsClaim, 1);
@@ -501,27 +558,29 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         const int w = item_at(k);
         if (w >= num_items) break;
         const ItemInfo it = load_item(p, work, w);
+        const int t0 = first_tile<kSplit>(it.ntiles), t1 = end_tile<kSplit>(it.ntiles);
+        if (kSplit && t0 == t1) continue;  // fewer tiles than CTAs: no Q comes
         ok = wait_bar(bar(kBarQReady), k & 1, abort_flag, status);
         const uint32_t g_first = g;
-        for (int t = 0; t < it.ntiles && ok; ++t, ++g) {
+        for (int t = t0; t < t1 && ok; ++t, ++g) {
           ok = wait_bar(bar(kBarKFull + g % kKStages), (g / kKStages) & 1, abort_flag, status);
-          if (ok && t > 0)
+          if (ok && t > t0)
             ok = wait_bar(bar(kBarVFull + (g - 1) % kVStages), ((g - 1) / kVStages) & 1, abort_flag,
                           status);
           if (!ok) break;
           tc_fence_after();
           for (int h = 0; h < 2 && ok; ++h) {
-            if (t > 0) issue_pv(h, g - 1, g - 1 == g_first);  // P_h of the previous tile
+            if (t > t0) issue_pv(h, g - 1, g - 1 == g_first);  // P_h of the previous tile
             if (ok) issue_qk(h, g);
           }
           if (ok && elect_one()) {
             umma_commit(bar(kBarKEmpty + g % kKStages));
-            if (t > 0) umma_commit(bar(kBarVEmpty + (g - 1) % kVStages));
-            if (t == it.ntiles - 1) umma_commit(bar(kBarQEmpty));
+            if (t > t0) umma_commit(bar(kBarVEmpty + (g - 1) % kVStages));
+            if (t == t1 - 1) umma_commit(bar(kBarQEmpty));
           }
           __syncwarp();
         }
-        if (ok && it.ntiles > 0) {  // P.V of the item's last tile
+        if (ok && t1 > t0) {  // P.V of the item's last tile
           const uint32_t gl = g - 1;
           ok = wait_bar(bar(kBarVFull + gl % kVStages), (gl / kVStages) & 1, abort_flag, status);
           if (ok) tc_fence_after();
@@ -551,6 +610,8 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
     // exponent of its largest value, as far as 2^-e is a normal number); sets the
     // scale of the row's scores
     float sl2_next = 0.f;
+    bool part = false;  // in a cluster: this CTA has one, and its rows' max and sum
+    float part_m = -INFINITY, part_l = 0.f;
     auto convert_q = [&](int k) {
       ok = wait_bar(bar(kBarQFull), k & 1, abort_flag, status);
       ok = __all_sync(0xffffffffu, ok);
@@ -585,11 +646,20 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       __syncwarp();
       if (elect_one()) mbar_arrive(bar(kBarQReady));
     };
-    if (item_at(0) < num_items) convert_q(0);
+    {
+      const int w = item_at(0);
+      bool any = w < num_items;
+      if (kSplit && any) {
+        const int n = load_item(p, work, w).ntiles;
+        any = first_tile<kSplit>(n) < end_tile<kSplit>(n);
+      }
+      if (any) convert_q(0);
+    }
     for (int k = 0; ok; ++k) {
       const int w = item_at(k);
       if (w >= num_items) break;
       const ItemInfo it = load_item(p, work, w);
+      const int t0 = first_tile<kSplit>(it.ntiles), t1 = end_tile<kSplit>(it.ntiles);
       const int head = pair_heads ? it.head0 + h : it.head0;
       const int qt = pair_heads ? it.qt0 : it.qt0 + h;
       const int jq = qt * QT + row;
@@ -599,7 +669,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       const float sl2 = sl2_next;
       float m_run = -INFINITY, l_run = 0.f;
       const uint32_t g_first = g;
-      for (int t = 0; t < it.ntiles && ok; ++t, ++g) {
+      for (int t = t0; t < t1 && ok; ++t, ++g) {
         // S_h of tile g is complete; so is P.V of tile g-1 (issued before it)
         ok = wait_bar(bar(kBarSFull + h), g & 1, abort_flag, status);
         if (!ok) break;
@@ -693,6 +763,12 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         __syncwarp();
         if (elect_one()) mbar_arrive(bar(kBarPFull + h));
       }
+      if constexpr (kSplit) {
+        if (ok && t1 > t0) ok = part = wait_bar(bar(kBarODone + h), (g - 1) & 1, abort_flag, status);
+        part_m = m_run;
+        part_l = l_run;
+        continue;
+      }
       // the next item's Q while this one's last P.V runs
       if (ok && item_at(k + 1) < num_items) convert_q(k + 1);
       if (!ok || it.ntiles == 0) continue;
@@ -723,6 +799,29 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       // the next item's first P.V overwrites O: every lane has read it
       tc_fence_before();
     }
+    if constexpr (kSplit) {
+      // ---- this CTA's part of O, and each row's max and sum, where K and V were
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // the other half's MMAs too
+      tc_fence_after();
+      part = __all_sync(0xffffffffu, part);
+      const int r = h * QT + row;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t orr[32];
+        tmem_ld32(tO + c * 32, orr);
+        tmem_ld_wait();
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(part_at<D>(sK, r, 8 * c + v)),
+                       "r"(part ? orr[4 * v] : 0u), "r"(part ? orr[4 * v + 1] : 0u),
+                       "r"(part ? orr[4 * v + 2] : 0u), "r"(part ? orr[4 * v + 3] : 0u)
+                       : "memory");
+      }
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(part_ml<D>(sK, r)), "f"(part_m),
+                   "f"(part_l)
+                   : "memory");
+      tc_fence_before();
+    }
   }
 
   // ---- wind down: every role is done (or gave up); free TMEM
@@ -733,6 +832,50 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
   if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+
+  if constexpr (kSplit) {
+    // ---- the parts of the cluster's CTAs joined, an equal share of the rows each
+    const int ctas = cluster_ctas(), w = (int)blockIdx.x / ctas;
+    __syncwarp();
+    cluster_sync();
+    if (warp < 8 && w < num_items) {  // (the others keep too few registers)
+      const ItemInfo it = load_item(p, work, w);
+      constexpr int kUnits = D / 4;
+      const int rows = 2 * QT / ctas, row0 = cluster_rank() * rows;
+      for (int i = threadIdx.x; i < rows * kUnits; i += 256) {
+        const int r = row0 + i / kUnits, u = i % kUnits, h = r / QT;
+        const int head = pair_heads ? it.head0 + h : it.head0;
+        const int jq = (pair_heads ? it.qt0 : it.qt0 + h) * QT + r % QT;
+        if (jq >= it.ql) continue;
+        float m = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < ctas; ++c) {
+          float mc, lc, o[4];
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                       : "=f"(mc), "=f"(lc)
+                       : "r"(in_cta(part_ml<D>(sK, r), c)));
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
+                       : "r"(in_cta(part_at<D>(sK, r, u), c)));
+          // (a part without a key that the row sees, or whose scores are all NaN,
+          // has no maximum: its O is 0, or NaN)
+          const float top = fmaxf(m, mc);
+          const float a = m == top ? 1.f : ex2(m - top), b = mc == -INFINITY ? 0.f : ex2(mc - top);
+          m = top;
+          l = l * a + lc * b;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = fmaf(o[e], b, y[e] * a);
+        }
+        const float inv = v_scale / l;
+        uint2 pk;
+        pk.x = pack_bf16x2(y[0] * inv, y[1] * inv);
+        pk.y = pack_bf16x2(y[2] * inv, y[3] * inv);
+        *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out +
+                                  ((int64_t)(it.q0 + jq) * p.num_q_heads + head) * D + 4 * u) = pk;
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // the others have read this CTA's shared memory
   }
 }
 
@@ -750,12 +893,9 @@ cudaError_t launch_d(const AttnParams& p, float v_scale, int max_query_len,
   cudaError_t e = prefill_work_list(&work, &upper, p, max_query_len, -1, seq_lens_host,
                                     query_start_loc_host, pair_heads, stream);
   if (e != cudaSuccess) return e;
-  auto kernel = prefill_fp4_kernel<D>;
   const int smem = Layout<D>::total;
-  static std::atomic<int> smem_done[64];
-  e = raise_smem_limit(kernel, smem, smem_done);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
+  static std::atomic<int> smem_done[64], split_smem_done[64];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
@@ -765,10 +905,38 @@ cudaError_t launch_d(const AttnParams& p, float v_scale, int max_query_len,
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  // items: those of the list, or what the step's sizes allow
+  const int64_t most = min((int64_t)p.num_seqs * ((max_query_len + QT - 1) / QT),
+                           (int64_t)p.num_tokens / QT + p.num_seqs) *
+                       (pair_heads ? p.num_q_heads / 2 : p.num_q_heads);
+  const int64_t items = work.count > 0 ? work.count : most;
+  const int tiles = work.count > 0 ? work.items[0].w : (p.max_seq_len + KT - 1) / KT;
+  const int ctas = prefill_fp4_cluster((double)items, tiles, max_ctas);
+  if (ctas > 1) {
+    auto kernel = prefill_fp4_kernel<D, true>;
+    e = raise_smem_limit(kernel, smem, split_smem_done);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)(items * ctas));
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p, v_scale, tq, pair_heads, work);
+  }
+  auto kernel = prefill_fp4_kernel<D, false>;
+  e = raise_smem_limit(kernel, smem, smem_done);
+  if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, kernel, p, v_scale, tq, pair_heads, work);
 }
 
 }  // namespace
+
+int prefill_fp4_cluster(double items, double tiles, int sms) {
+  int n = 1;
+  if (sms < device_sm_count()) return n;  // beside the decode kernel
+  while (n < kMaxCluster && items * (2 * n) <= sms && tiles >= 4 * n) n *= 2;
+  return n;
+}
 
 cudaError_t launch_prefill_fp4(const AttnParams& p, float v_scale, int head_dim,
                                int max_query_len, const int32_t* seq_lens_host,

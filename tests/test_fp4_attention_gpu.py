@@ -170,6 +170,29 @@ def test_long_contexts_over_many_processors(hq, hkv, d, lens):
 
 
 @pytest.mark.parametrize("hq,hkv,d,lens,qls", [
+    (8, 1, 128, [9000], [640]),              # 20 items of 71 tiles: four CTAs each
+    (32, 8, 128, [5000], [512]),             # 64 items: two
+    (4, 2, 128, [3001], [700]),              # 12: eight
+    (4, 4, 64, [7777], [600]),               # heads that do not pair up, D = 64
+    (3, 1, 64, [4000, 77], [513, 40]),       # and a short chunk's items beside: some
+    (16, 2, 64, [6000, 600], [300, 600]),    # of a cluster's CTAs have no tile
+])
+def test_chunks_whose_keys_are_cut(hq, hkv, d, lens, qls):
+    st = Step(sum(lens) + d, lens, qls, hq, hkv, d)
+    a = st.run()
+    st.check(a)
+    b = st.run(host=True)
+    st.check(b)
+    assert torch.equal(a, st.run()) and torch.equal(b, st.run(host=True))
+    # a NaN or an infinity stays in its row
+    st.q[qls[0] // 2, 1, 9], st.q[5, 0, 0] = float("nan"), float("inf")
+    got = st.run(host=True)
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[qls[0] // 2, 1] = bad[5, 0] = True
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], b[~bad])
+
+
+@pytest.mark.parametrize("hq,hkv,d,lens,qls", [
     (16, 1, 128, [8727] * 5, [1] * 5),                # 30 processors a unit
     (8, 1, 64, [8270, 33083], [1, 1]),                # 30 and 118
     (16, 1, 64, [9000, 21000, 5], [4, 2, 1]),         # several units of one sequence
