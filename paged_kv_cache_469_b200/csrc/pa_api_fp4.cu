@@ -124,7 +124,6 @@ Fp4Costs fp4_costs(int head_dim) {
   return head_dim == 128 ? Fp4Costs{{60., 93.}, 1950., 24, 44} : Fp4Costs{{38., 50.}, 1800., 36, 72};
 }
 constexpr double kLaunchNs = 8000.;  // a kernel's start and end
-constexpr double kJoinNs = 4000.;    // and the join of an item's parts
 
 // The prefill kernel's work of a step.
 struct PrefillLoad {
@@ -133,7 +132,7 @@ struct PrefillLoad {
   double ns(int n, double tile_ns) const {
     if (items <= 0.) return 0.;
     const int ctas = prefill_fp4_cluster(items, longest, n);  // of an item
-    if (ctas > 1) return tile_ns * ceil(longest / ctas) + kLaunchNs + kJoinNs;
+    if (ctas > 1) return tile_ns * (ceil(longest / ctas) + kPrefillJoinTiles) + kLaunchNs;
     return tile_ns * (items <= n ? longest : max(longest, tiles / n + longest / 2)) + kLaunchNs;
   }
 };
@@ -147,9 +146,10 @@ struct Fp4Split {
 };
 
 // Divides a step's sequences between the kernels by their query tokens.  Few
-// prefill items leave most SMs idle, whatever their length: one chunk of 64 tokens
-// over 32768 keys (32 + 8 heads of 128) takes 500 us there and 169 here.  Without
-// the host copies a step is taken for one of equal lengths.
+// prefill items leave SMs idle even with their keys cut: one chunk of 64 tokens (32 +
+// 8 heads of 128) over 32768 keys takes 100 us there (500 uncut) and 160 on the decode
+// kernel, one of 48 over 4096 about 41 and 30.  Without the host copies a step is
+// taken for one of equal lengths.
 Fp4Split fp4_split(int num_seqs, int num_tokens, int max_query_len, int max_seq_len,
                    int num_q_heads, int num_kv_heads, int head_dim, const int32_t* seq_lens_host,
                    const int32_t* query_start_loc_host) {

@@ -262,8 +262,9 @@ cudaError_t launch_prefill_tcgen05(const AttnParams& p, int head_dim, int max_qu
                                    int max_ctas);
 
 // CTAs of a cluster that shares an item of launch_prefill_fp4 on `sms` SMs, for that
-// many items of at most that many 128-key tiles: as many as leave every item a
-// cluster at once and every CTA two tiles.
+// many items of at most that many 128-key tiles: those that end soonest, as long as
+// every item has a cluster at once and their join pays.
+constexpr double kPrefillJoinTiles = 3.;  // what the join takes, in tiles
 int prefill_fp4_cluster(double items, double tiles, int sms);
 
 // The same over a 4-bit cache (p.k_cache): p.scale_log2 holds its k_scale.

@@ -35,8 +35,9 @@
 // Fewer items than half the SMs are cut along their keys: a cluster of two to eight
 // CTAs takes an item, each an equal stretch of its tiles, and each joins an equal
 // share of its rows from the others' shared memory.  One chunk of 512 over 8192
-// tokens, 64 items: 89 us, 133 without; two of 247 over up to 2953 on one kv-head,
-// 32 items: 27.8, 53.7 without.
+// tokens, 64 items: 77.5 us, 133 without; two of 247 over up to 2953 on one kv-head,
+// 32 items: 26.2, 53.7 without.  (The join takes 5 us; parts stored to the CTA that
+// joins them, 16 bytes a lane, instead of loaded by it: 79.5 and 29.)
 //
 // Every mbarrier wait is bounded by a time limit; a wait that runs out sets a
 // status bit in the workspace and the CTA winds down instead of hanging.
@@ -610,8 +611,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
     // exponent of its largest value, as far as 2^-e is a normal number); sets the
     // scale of the row's scores
     float sl2_next = 0.f;
-    bool part = false;  // in a cluster: this CTA has one, and its rows' max and sum
-    float part_m = -INFINITY, part_l = 0.f;
+    float m_run = -INFINITY, l_run = 0.f;  // this row's running max and sum
     auto convert_q = [&](int k) {
       ok = wait_bar(bar(kBarQFull), k & 1, abort_flag, status);
       ok = __all_sync(0xffffffffu, ok);
@@ -667,7 +667,8 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       const int pos = row_valid ? it.L - it.ql + jq : -1;  // last visible key
       const int min_pos = it.L - it.ql + qt * QT;          // smallest position in the tile
       const float sl2 = sl2_next;
-      float m_run = -INFINITY, l_run = 0.f;
+      m_run = -INFINITY;
+      l_run = 0.f;
       const uint32_t g_first = g;
       for (int t = t0; t < t1 && ok; ++t, ++g) {
         // S_h of tile g is complete; so is P.V of tile g-1 (issued before it)
@@ -764,10 +765,8 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         if (elect_one()) mbar_arrive(bar(kBarPFull + h));
       }
       if constexpr (kSplit) {
-        if (ok && t1 > t0) ok = part = wait_bar(bar(kBarODone + h), (g - 1) & 1, abort_flag, status);
-        part_m = m_run;
-        part_l = l_run;
-        continue;
+        if (ok && t1 > t0) ok = wait_bar(bar(kBarODone + h), (g - 1) & 1, abort_flag, status);
+        break;  // one item to a cluster
       }
       // the next item's Q while this one's last P.V runs
       if (ok && item_at(k + 1) < num_items) convert_q(k + 1);
@@ -803,7 +802,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       // ---- this CTA's part of O, and each row's max and sum, where K and V were
       asm volatile("bar.sync 1, 256;" ::: "memory");  // the other half's MMAs too
       tc_fence_after();
-      part = __all_sync(0xffffffffu, part);
+      const bool part = __all_sync(0xffffffffu, ok && g > 0);
       const int r = h * QT + row;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -817,8 +816,8 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
                        "r"(part ? orr[4 * v + 2] : 0u), "r"(part ? orr[4 * v + 3] : 0u)
                        : "memory");
       }
-      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(part_ml<D>(sK, r)), "f"(part_m),
-                   "f"(part_l)
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(part_ml<D>(sK, r)), "f"(m_run),
+                   "f"(l_run)
                    : "memory");
       tc_fence_before();
     }
@@ -841,37 +840,56 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
     cluster_sync();
     if (warp < 8 && w < num_items) {  // (the others keep too few registers)
       const ItemInfo it = load_item(p, work, w);
-      constexpr int kUnits = D / 4;
-      const int rows = 2 * QT / ctas, row0 = cluster_rank() * rows;
-      for (int i = threadIdx.x; i < rows * kUnits; i += 256) {
-        const int r = row0 + i / kUnits, u = i % kUnits, h = r / QT;
-        const int head = pair_heads ? it.head0 + h : it.head0;
-        const int jq = (pair_heads ? it.qt0 : it.qt0 + h) * QT + r % QT;
-        if (jq >= it.ql) continue;
-        float m = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int c = 0; c < ctas; ++c) {
-          float mc, lc, o[4];
-          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                       : "=f"(mc), "=f"(lc)
-                       : "r"(in_cta(part_ml<D>(sK, r), c)));
-          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
-                       : "r"(in_cta(part_at<D>(sK, r, u), c)));
-          // (a part without a key that the row sees, or whose scores are all NaN,
-          // has no maximum: its O is 0, or NaN)
-          const float top = fmaxf(m, mc);
-          const float a = m == top ? 1.f : ex2(m - top), b = mc == -INFINITY ? 0.f : ex2(mc - top);
-          m = top;
-          l = l * a + lc * b;
+      constexpr int kUnits = D / 4, kRows = 2;  // (rows of a thread at once)
+      const int rank = cluster_rank(), row0 = rank * 2 * QT / ctas;
+      const int row1 = (rank + 1) * 2 * QT / ctas, u = threadIdx.x % kUnits;
+      for (int r0 = row0 + threadIdx.x / kUnits; r0 < row1; r0 += kRows * 256 / kUnits) {
+        int r[kRows];
+        float m[kRows], l[kRows], y[kRows][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = fmaf(o[e], b, y[e] * a);
+        for (int e = 0; e < kRows; ++e) {
+          r[e] = min(r0 + e * 256 / kUnits, row1 - 1);
+          m[e] = -INFINITY;
+          l[e] = y[e][0] = y[e][1] = y[e][2] = y[e][3] = 0.f;
         }
-        const float inv = v_scale / l;
-        uint2 pk;
-        pk.x = pack_bf16x2(y[0] * inv, y[1] * inv);
-        pk.y = pack_bf16x2(y[2] * inv, y[3] * inv);
-        *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out +
-                                  ((int64_t)(it.q0 + jq) * p.num_q_heads + head) * D + 4 * u) = pk;
+#pragma unroll 2
+        for (int i = 0; i < ctas; ++i) {  // (each CTA begins with its own part)
+          const int c = rank + i < ctas ? rank + i : rank + i - ctas;
+          float mc[kRows], lc[kRows], o[kRows][4];
+#pragma unroll
+          for (int e = 0; e < kRows; ++e) {
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                         : "=f"(mc[e]), "=f"(lc[e])
+                         : "r"(in_cta(part_ml<D>(sK, r[e]), c)));
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(o[e][0]), "=f"(o[e][1]), "=f"(o[e][2]), "=f"(o[e][3])
+                         : "r"(in_cta(part_at<D>(sK, r[e], u), c)));
+          }
+#pragma unroll
+          for (int e = 0; e < kRows; ++e) {
+            // (a part without a key that the row sees, or whose scores are all NaN,
+            // has no maximum: its O is 0, or NaN)
+            const float top = fmaxf(m[e], mc[e]);
+            const float f = m[e] == top ? 1.f : ex2(m[e] - top);
+            const float fc = mc[e] == -INFINITY ? 0.f : ex2(mc[e] - top);
+            m[e] = top;
+            l[e] = l[e] * f + lc[e] * fc;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[e][k] = fmaf(o[e][k], fc, y[e][k] * f);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kRows; ++e) {
+          const int h = r[e] / QT, head = pair_heads ? it.head0 + h : it.head0;
+          const int jq = (pair_heads ? it.qt0 : it.qt0 + h) * QT + r[e] % QT;
+          if (jq >= it.ql || r0 + e * 256 / kUnits >= row1) continue;
+          const float inv = v_scale / l[e];
+          uint2 pk;
+          pk.x = pack_bf16x2(y[e][0] * inv, y[e][1] * inv);
+          pk.y = pack_bf16x2(y[e][2] * inv, y[e][3] * inv);
+          *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out +
+                                    ((int64_t)(it.q0 + jq) * p.num_q_heads + head) * D + 4 * u) = pk;
+        }
       }
     }
     __syncwarp();
@@ -931,11 +949,45 @@ cudaError_t launch_d(const AttnParams& p, float v_scale, int max_query_len,
 
 }  // namespace
 
+// Clusters of n CTAs that the device holds at once, asked for once per device (74
+// of two, 33 of four, 15 of eight at 148 SMs); 0 if it does not say
+static int resident_clusters(int n) {
+  static std::atomic<int> known[64][kMaxCluster + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int held = known[dev][n].load(std::memory_order_relaxed);
+  if (held == 0) {
+    static std::atomic<int> smem_done[64];
+    auto kernel = prefill_fp4_kernel<128, true>;
+    if (raise_smem_limit(kernel, Layout<128>::total, smem_done) != cudaSuccess) return 0;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Layout<128>::total;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&held, kernel, &cfg) != cudaSuccess) return 0;
+    known[dev][n].store(held, std::memory_order_relaxed);
+  }
+  return held;
+}
+
 int prefill_fp4_cluster(double items, double tiles, int sms) {
-  int n = 1;
-  if (sms < device_sm_count()) return n;  // beside the decode kernel
-  while (n < kMaxCluster && items * (2 * n) <= sms && tiles >= 4 * n) n *= 2;
-  return n;
+  int best = 1;
+  if (sms < device_sm_count() || 2 * items > sms) return best;  // beside the decode kernel; full
+  double best_cost = tiles;
+  for (int n = 2; n <= kMaxCluster && items * n <= sms; ++n) {
+    const double cost = ceil(tiles / n) + kPrefillJoinTiles;
+    if (cost < best_cost && items <= resident_clusters(n)) {
+      best_cost = cost;
+      best = n;
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_prefill_fp4(const AttnParams& p, float v_scale, int head_dim,
