@@ -15,9 +15,9 @@
 // once to the row's type, or to a 4-bit group.
 //
 // Quantisation of 16 dims x of one token: s = e4m3(min(max|x| / (6 g), 448)),
-// codes e2m1(x / (s g)), g the tensor's scale.  Both divisions are IEEE ones:
+// codes e2m1(x / (s g)), g the tensor's scale.  Both quotients are rounded as IEEE's:
 // a value half-way between two codes then goes to the even code, where a
-// product with a rounded reciprocal would send it either way.  A NaN makes its
+// product with a rounded reciprocal alone would send it either way.  A NaN makes its
 // group's scale NaN.
 //
 // Bound: HBM bytes for prompts, latency for a few tokens.  A lane holds two
@@ -102,13 +102,31 @@ __device__ __forceinline__ uint32_t group_scale(float amax, float six_g) {
 // eight codes under that scale, dim 2j in the low half of byte j
 __device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t scale, float g) {
   const float product = __fmul_rn(e4m3_to_float(scale), g);
-  const float d = product > 0.f ? product : INFINITY;
+  float y[8];
+  // One correctly rounded reciprocal and two residual steps give each quotient as the
+  // division rounds it (Markstein 1990: q + (x - q d) RN(1 / d) rounds right from a q
+  // within a unit of the last place), where nothing overflows and no residual that
+  // matters underflows: scales that neither saturate nor are NaN (quotients below 16),
+  // tensor scales of middle size.  4099 tokens of 32 + 2 x 8 heads of 128: 23.7 us, with
+  // a division per value 24.7.
+  if (scale < 126 && (product == 0.f || (product >= 0x1p-60f && product <= 0x1p60f))) {
+    const float r = product > 0.f ? __frcp_rn(product) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float q = __fmul_rn(x[i], r);
+      q = fmaf(fmaf(-q, product, x[i]), r, q);
+      y[i] = fmaf(fmaf(-q, product, x[i]), r, q);
+    }
+  } else {
+    const float d = product > 0.f ? product : INFINITY;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], d);
+  }
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w |= (uint32_t)__nv_cvt_float2_to_fp4x2(
-             make_float2(__fdiv_rn(x[2 * i], d), __fdiv_rn(x[2 * i + 1], d)), __NV_E2M1,
-             cudaRoundNearest)
+    w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(y[2 * i], y[2 * i + 1]), __NV_E2M1,
+                                            cudaRoundNearest)
          << (8 * i);
   return w;
 }

@@ -149,6 +149,34 @@ def test_rope_append_fp4_bytes_and_gather(tokens, hq, hkv, d, dtype, r, interlea
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("g", [1.0, 0.37, 3.3e-4, 2.0 ** -61, 1.7e-30, 2.0 ** 59, 4.1e25])
+def test_quantiser_next_to_its_ties(g):
+    """Values on both sides of every border between two codes, one and two units of the
+    last place off it, under every scale and tensor scales of any size."""
+    rng = np.random.default_rng(int(abs(np.log2(g)) * 7))
+    tokens, d, g = 1000, 128, np.float32(g)
+    scale = fp4_side.E4M3[rng.integers(8, 126, (tokens, d // 16))].astype(np.float32)
+    with np.errstate(over="ignore", invalid="ignore"):
+        unit = (scale * g)[..., None]
+        ties = np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5], np.float32)
+        x = ties[rng.integers(0, 7, (tokens, d // 16, 16))] * unit
+        for _ in range(2):
+            off = rng.integers(-1, 2, x.shape)
+            x = np.where(off == 0, x, np.nextafter(x, np.float32(np.inf) * off, dtype=np.float32))
+        x[..., 3:4] = 6 * unit
+    x = (x * rng.choice(np.array([-1, 1], np.float32), x.shape)).reshape(tokens, 1, d)
+    assert np.isfinite(x).all()
+    rows, cache = torch.from_numpy(x).cuda(), lib.new_fp4_cache(63, 1, d)
+    lib.rope_append_fp4(rows[:, :0], rows, rows, cache, torch.arange(tokens, device="cuda"), None,
+                        None, k_scale=float(g), v_scale=float(g))
+    want = np.zeros((63, 1, 18 * d), np.uint8)
+    c, s = fp4_side.quantise(x, g)
+    for i in range(tokens):
+        fp4_side.put_row(want[i // 16, 0], i % 16, d, c[i, 0], s[i, 0], c[i, 0], s[i, 0])
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+
+@pytest.mark.gpu
 def test_quantiser_at_its_borders():
     """Exact ties, values at and past the largest, zeros, subnormal scales, infinities
     and NaN."""
