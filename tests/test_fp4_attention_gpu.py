@@ -192,6 +192,36 @@ def test_chunks_whose_keys_are_cut(hq, hkv, d, lens, qls):
     assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], b[~bad])
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(8, 1, 128), (4, 4, 64), (8, 2, 64)])
+def test_cut_keys_follow_the_device_lengths(hq, hkv, d):
+    """Bounds far above the lengths: more CTAs share a chunk's keys than it has tiles.
+    The same captured call, as the lengths grow, and on two streams at once."""
+    lens = np.array([300, 140], np.int32)
+    st = Step(hq + d, [9000, 6000], [256, 129], hq, hkv, d, junk=False)
+    full = st.lens.copy()
+    st.dev[1].copy_(torch.from_numpy(lens))
+    graph, out = torch.cuda.CUDAGraph(), torch.full_like(st.q, float("nan"))
+    with torch.cuda.graph(graph):
+        st.run(out=out)
+    for now in (lens, np.array([2000, 6000], np.int32), full, lens):
+        st.lens = now
+        st.dev[1].copy_(torch.from_numpy(now))
+        out.fill_(float("nan"))
+        graph.replay()
+        st.check(out)
+    other = Step(hq + d + 1, [5000], [200], hq, hkv, d)
+    want = [out.clone(), other.run()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [torch.full_like(w, float("nan")) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, step, o in zip(streams, (st, other), got):
+            with torch.cuda.stream(s):
+                step.run(out=o)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("hq,hkv,d,lens,qls", [
     (16, 1, 128, [8727] * 5, [1] * 5),                # 30 processors a unit
     (8, 1, 64, [8270, 33083], [1, 1]),                # 30 and 118
