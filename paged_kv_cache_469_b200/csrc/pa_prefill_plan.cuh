@@ -67,48 +67,58 @@ prefill_plan_kernel(const AttnParams p, int max_tiles, int pair_heads) {
   for (int i = threadIdx.x; i <= max_tiles; i += blockDim.x) hist[i] = 0;
   __syncthreads();
   const int per_tile = pair_heads ? p.num_q_heads / 2 : p.num_q_heads;  // items per (seq, tile)
+  const int lane = threadIdx.x & 31;
+  // fn(sequence, item of it, key tiles): a lane reads a sequence, and its warp goes
+  // over the items of those that have any
+  auto for_each_item = [&](auto fn) {
+    for (int s0 = threadIdx.x - lane; s0 < p.num_seqs; s0 += blockDim.x) {
+      int ql = 0, L = 0;
+      if (s0 + lane < p.num_seqs) {
+        ql = p.query_start_loc[s0 + lane + 1] - p.query_start_loc[s0 + lane];
+        L = p.seq_lens[s0 + lane];
+      }
+      const bool mine = !(ql * p.group <= p.decode_max_rows || ql > L);
+      for (unsigned left = __ballot_sync(0xffffffffu, mine); left; left &= left - 1) {
+        const int from = __ffs(left) - 1;
+        const int ql1 = __shfl_sync(0xffffffffu, ql, from), L1 = __shfl_sync(0xffffffffu, L, from);
+        const int nq = (ql1 + QT - 1) / QT;
+        const int ni = pair_heads ? nq : (nq + 1) / 2;
+        for (int i = lane; i < ni; i += 32) {
+          int last;
+          prefill_item_range(L1, ql1, pair_heads, i, &last);
+          fn(s0 + from, i, min(last / KT + 1, max_tiles));
+        }
+      }
+    }
+  };
   // pass 1: histogram of items by tile count
-  for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
-    const int q0 = p.query_start_loc[s], ql = p.query_start_loc[s + 1] - q0, L = p.seq_lens[s];
-    if (ql * p.group <= p.decode_max_rows || ql > L) continue;
-    const int nq = (ql + QT - 1) / QT;
-    const int ni = pair_heads ? nq : (nq + 1) / 2;
-    for (int i = 0; i < ni; ++i) {
-      int last;
-      prefill_item_range(L, ql, pair_heads, i, &last);
-      const int nt = min(last / KT + 1, max_tiles);
-      atomicAdd(&hist[nt], per_tile);
-    }
-  }
+  for_each_item([&](int, int, int nt) { atomicAdd(&hist[nt], per_tile); });
   __syncthreads();
-  if (threadIdx.x == 0) {  // exclusive offsets, descending tile count
+  if (threadIdx.x < 32) {  // exclusive offsets, descending tile count
     int run = 0;
-    for (int nt = max_tiles; nt >= 0; --nt) {
-      const int c = hist[nt];
-      hist[nt] = run;
-      run += c;
+    for (int hi = max_tiles; hi >= 0; hi -= 32) {
+      const int nt = hi - lane;
+      const int c = nt >= 0 ? hist[nt] : 0;
+      int sum = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      if (nt >= 0) hist[nt] = run + sum - c;
+      run += __shfl_sync(0xffffffffu, sum, 31);
     }
-    p.ws_items[0] = make_int4(min(run, p.max_items), 0, 0, 0);
+    if (lane == 0) p.ws_items[0] = make_int4(min(run, p.max_items), 0, 0, 0);
   }
   __syncthreads();
   // pass 2: scatter
-  for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
-    const int q0 = p.query_start_loc[s], ql = p.query_start_loc[s + 1] - q0, L = p.seq_lens[s];
-    if (ql * p.group <= p.decode_max_rows || ql > L) continue;
-    const int nq = (ql + QT - 1) / QT;
-    const int ni = pair_heads ? nq : (nq + 1) / 2;
-    for (int i = ni - 1; i >= 0; --i) {
-      int last;
-      prefill_item_range(L, ql, pair_heads, i, &last);
-      const int nt = min(last / KT + 1, max_tiles);
-      const int at = atomicAdd(&hist[nt], per_tile);
-      for (int h = 0; h < per_tile; ++h) {
-        if (at + h >= p.max_items) break;
-        p.ws_items[1 + at + h] = pair_heads ? make_int4(s, i, 2 * h, nt)
-                                            : make_int4(s, 2 * i, h, nt);
-      }
+  for_each_item([&](int s, int i, int nt) {
+    const int at = atomicAdd(&hist[nt], per_tile);
+    for (int h = 0; h < per_tile; ++h) {
+      if (at + h >= p.max_items) break;
+      p.ws_items[1 + at + h] = pair_heads ? make_int4(s, i, 2 * h, nt) : make_int4(s, 2 * i, h, nt);
     }
-  }
+  });
 }
 
 // The work list of prefill_plan_kernel, built on the host from its copies of
