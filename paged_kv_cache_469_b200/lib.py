@@ -294,9 +294,11 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torc
     projection are fine); caches: [num_blocks, Hkv, 16, D]; slot_mapping,
     positions: int64 [T]; cos_sin: float32 [max_position, rotary_dim], the
     cosines and then the sines of a position's angles (None: nothing is
-    rotated).  Returns q_out (a new tensor unless given)."""
+    rotated).  Returns q_out (a new tensor unless given, one of ``stream``: what
+    is made by a call belongs to the stream that writes it)."""
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        with torch.cuda.stream(stream):
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     rc = _marshal().rope_append(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out,
                                 interleaved, None if stream is None else stream.cuda_stream)
     if rc != PA_OK:
@@ -319,7 +321,8 @@ def rope_append_fp4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_cache:
     """``rope_append`` into a 4-bit cache (see pa_rope_append_fp4 in pa.h); k_scale and
     v_scale are the tensors' own scales."""
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        with torch.cuda.stream(stream):
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     rc = _marshal().rope_append_fp4(q, k, v, kv_cache, k_scale, v_scale, slot_mapping, positions,
                                     cos_sin, q_out, interleaved,
                                     None if stream is None else stream.cuda_stream)
@@ -335,10 +338,11 @@ def gather_fp4(kv_cache: torch.Tensor, slots: torch.Tensor, *, k_scale: float = 
     of slots outside the pool are left as they are (see pa_gather_fp4 in pa.h)."""
     if k_out is None or v_out is None:
         shape = (slots.shape[0], kv_cache.shape[1], kv_cache.shape[2] // 18)
-        if k_out is None:
-            k_out = torch.zeros(shape, dtype=dtype, device=kv_cache.device)
-        if v_out is None:
-            v_out = torch.zeros(shape, dtype=k_out.dtype, device=kv_cache.device)
+        with torch.cuda.stream(stream):  # the fills come before the gather
+            if k_out is None:
+                k_out = torch.zeros(shape, dtype=dtype, device=kv_cache.device)
+            if v_out is None:
+                v_out = torch.zeros(shape, dtype=k_out.dtype, device=kv_cache.device)
     rc = _marshal().gather_fp4(kv_cache, slots, k_scale, v_scale, k_out, v_out,
                                None if stream is None else stream.cuda_stream)
     if rc != PA_OK:
@@ -353,7 +357,8 @@ def new_fp4_workspace(num_seqs: int, num_tokens: int, num_q_heads: int, num_kv_h
                                                       num_kv_heads, head_dim))
     if n == 0:
         raise ValueError("invalid workspace bounds")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
     if not ws.is_cuda:
         raise ValueError("the workspace must be on a CUDA device")
     with torch.cuda.device(ws.device):
