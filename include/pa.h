@@ -440,11 +440,12 @@ size_t pa_attention_fp4_workspace_size(int num_seqs, int num_tokens, int num_q_h
  * with K, V the cache's values, and everything else as there (positions, heads,
  * block tables, bounds).  Slots of the last block past seq_lens[s] are never
  * used, whatever they hold; a block id outside the pool is never dereferenced.
- * dtype is that of q and out, which must not overlap.  The kernels plan the
- * step's work from the device arrays; the optional host copies are checked, and
- * decide which kernels run and on how many SMs: a captured call without them
- * follows whatever lengths the device arrays hold at its replay, one with them
- * needs query lengths of the same sequences.
+ * dtype is that of q and out, which must not overlap.  The kernels take the
+ * lengths from the device arrays; the optional host copies are checked, and
+ * decide which kernels run, on how many SMs and in what order they take the
+ * chunks: a captured call without them follows whatever lengths the device arrays
+ * hold at its replay, one with them whatever seq_lens they hold there (up to
+ * max_seq_len), with the query_start_loc of its capture.
  *
  * A sequence of few query tokens (by a rule on the step's sizes; all of an fp32
  * step) runs on a split-K kernel that reads the cache once per kv-head and 16

@@ -300,6 +300,17 @@ __device__ __forceinline__ int end_tile(int ntiles) {
   return kSplit ? (cluster_rank() + 1) * ntiles / cluster_ctas() : ntiles;
 }
 
+// An item of the list, with the key tiles that the device's lengths give it: a list
+// made on the host is as old as the captured call that it is part of.
+__device__ __forceinline__ ItemInfo item_now(const AttnParams& p, const PrefillWork& work, int w,
+                                             int pair_heads) {
+  ItemInfo it = load_item(p, work, w);
+  const int last_row = min((it.qt0 + (pair_heads ? 1 : 2)) * QT, it.ql) - 1;
+  const int wide = (p.max_blocks_per_seq + kTileBlocks - 1) / kTileBlocks;
+  it.ntiles = min(max(it.L - it.ql + last_row, 0) / KT + 1, wide);
+  return it;
+}
+
 // The tiles of a CTA's items one after the other, as the producers walk them
 template <bool kSplit>
 struct TileCursor {
@@ -310,8 +321,8 @@ struct TileCursor {
   bool done = false;
   // item(k): the place of this CTA's item k in the list, past its end if none
   template <typename Item>
-  __device__ __forceinline__ void next(const AttnParams& p, const PrefillWork& work, int num_items,
-                                       Item item) {
+  __device__ __forceinline__ void next(const AttnParams& p, const PrefillWork& work, int pair_heads,
+                                       int num_items, Item item) {
     if (done) return;
     while (++t >= ntiles) {
       w = item(++k);
@@ -319,7 +330,7 @@ struct TileCursor {
         done = true;
         return;
       }
-      const ItemInfo it = load_item(p, work, w);
+      const ItemInfo it = item_now(p, work, w, pair_heads);
       t = first_tile<kSplit>(it.ntiles) - 1;
       ntiles = end_tile<kSplit>(it.ntiles);
       kvh = it.head0 / p.group;
@@ -429,7 +440,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         if (kSplit) publish(1, INT32_MAX);  // one item to a cluster
       }
       TileCursor<kSplit> cur, nxt;
-      nxt.next(p, work, num_items, item_at);
+      nxt.next(p, work, pair_heads, num_items, item_at);
       int ids_n = nxt.ids(p, lane);
       auto tile_of = [&](int ids, int b, int kvh) -> const uint8_t* {
         const int id = __shfl_sync(0xffffffffu, ids, b & 7);
@@ -475,7 +486,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
           taken = (int)gridDim.x + atomicAdd(p.ws_header + kWsClaim, 1);
           if (cur.ntiles == 1) publish(cur.k + 1, taken);
         }
-        nxt.next(p, work, num_items, item_at);
+        nxt.next(p, work, pair_heads, num_items, item_at);
         ids_n = nxt.ids(p, lane);
         const int key0 = cur.t * KT;
 #pragma unroll
@@ -558,7 +569,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       for (int k = 0; ok; ++k) {
         const int w = item_at(k);
         if (w >= num_items) break;
-        const ItemInfo it = load_item(p, work, w);
+        const ItemInfo it = item_now(p, work, w, pair_heads);
         const int t0 = first_tile<kSplit>(it.ntiles), t1 = end_tile<kSplit>(it.ntiles);
         if (kSplit && t0 == t1) continue;  // fewer tiles than CTAs: no Q comes
         ok = wait_bar(bar(kBarQReady), k & 1, abort_flag, status);
@@ -650,7 +661,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       const int w = item_at(0);
       bool any = w < num_items;
       if (kSplit && any) {
-        const int n = load_item(p, work, w).ntiles;
+        const int n = item_now(p, work, w, pair_heads).ntiles;
         any = first_tile<kSplit>(n) < end_tile<kSplit>(n);
       }
       if (any) convert_q(0);
@@ -658,7 +669,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
     for (int k = 0; ok; ++k) {
       const int w = item_at(k);
       if (w >= num_items) break;
-      const ItemInfo it = load_item(p, work, w);
+      const ItemInfo it = item_now(p, work, w, pair_heads);
       const int t0 = first_tile<kSplit>(it.ntiles), t1 = end_tile<kSplit>(it.ntiles);
       const int head = pair_heads ? it.head0 + h : it.head0;
       const int qt = pair_heads ? it.qt0 : it.qt0 + h;
