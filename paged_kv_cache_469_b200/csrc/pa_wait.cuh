@@ -86,6 +86,17 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   }
 }
 
+// The same for a whole warp: true in every lane or in none.  (Lanes that look at the
+// limit or the abort flag at different times would part before the warp's collective
+// instructions.)
+__device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity,
+                                              volatile int* abort_flag, int* status,
+                                              unsigned long long limit_ns = kWaitLimitNs) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const bool ok = wait_bar(bar, parity, abort_flag, status, limit_ns);
+  return __all_sync(0xffffffffu, ok);
+}
+
 // What a role that gives up does before it returns, for its own copies and MMAs
 // still under way: waits for their phase whatever the abort flag says, until
 // limit_ns after t0.

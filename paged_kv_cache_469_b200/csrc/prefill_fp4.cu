@@ -412,7 +412,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
   // again eight items later, which every role must have reached by then.)
   auto item_at = [&](int k) {
     int w = INT32_MAX;
-    if (wait_bar(bar(kBarItem + k % kItemRing), (k / kItemRing) & 1, abort_flag, status))
+    if (wait_bar_warp(bar(kBarItem + k % kItemRing), (k / kItemRing) & 1, abort_flag, status))
       w = *(volatile int*)&sh_item[k % kItemRing];
     return __shfl_sync(0xffffffffu, w, 0);
   };
@@ -496,8 +496,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
           const int full = (phase ? kBarVFull : kBarKFull) + st;
           const int empty = (phase ? kBarVEmpty : kBarKEmpty) + st;
           if (g >= nst) {
-            ok = wait_bar(bar(empty), ((g / nst) - 1) & 1, abort_flag, status);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = wait_bar_warp(bar(empty), ((g / nst) - 1) & 1, abort_flag, status);
             if (!ok) break;
           }
           const uint32_t dst = phase ? sV + st * LY::kBytes + Share<D>::at_v(lane)
@@ -537,7 +536,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       uint32_t g = 0;
       bool ok = true;
       auto issue_pv = [&](int h, uint32_t gt, bool first_of_item) {  // O_h += P_h V (tile gt)
-        ok = wait_bar(bar(kBarPFull + h), gt & 1, abort_flag, status);
+        ok = wait_bar_warp(bar(kBarPFull + h), gt & 1, abort_flag, status);
         if (!ok) return;
         tc_fence_after();
         if (elect_one()) {
@@ -572,13 +571,13 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         const ItemInfo it = item_now(p, work, w, pair_heads);
         const int t0 = first_tile<kSplit>(it.ntiles), t1 = end_tile<kSplit>(it.ntiles);
         if (kSplit && t0 == t1) continue;  // fewer tiles than CTAs: no Q comes
-        ok = wait_bar(bar(kBarQReady), k & 1, abort_flag, status);
+        ok = wait_bar_warp(bar(kBarQReady), k & 1, abort_flag, status);
         const uint32_t g_first = g;
         for (int t = t0; t < t1 && ok; ++t, ++g) {
-          ok = wait_bar(bar(kBarKFull + g % kKStages), (g / kKStages) & 1, abort_flag, status);
+          ok = wait_bar_warp(bar(kBarKFull + g % kKStages), (g / kKStages) & 1, abort_flag, status);
           if (ok && t > t0)
-            ok = wait_bar(bar(kBarVFull + (g - 1) % kVStages), ((g - 1) / kVStages) & 1, abort_flag,
-                          status);
+            ok = wait_bar_warp(bar(kBarVFull + (g - 1) % kVStages), ((g - 1) / kVStages) & 1,
+                               abort_flag, status);
           if (!ok) break;
           tc_fence_after();
           for (int h = 0; h < 2 && ok; ++h) {
@@ -594,7 +593,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         }
         if (ok && t1 > t0) {  // P.V of the item's last tile
           const uint32_t gl = g - 1;
-          ok = wait_bar(bar(kBarVFull + gl % kVStages), (gl / kVStages) & 1, abort_flag, status);
+          ok = wait_bar_warp(bar(kBarVFull + gl % kVStages), (gl / kVStages) & 1, abort_flag, status);
           if (ok) tc_fence_after();
           for (int h = 0; h < 2 && ok; ++h) issue_pv(h, gl, gl == g_first);
           if (ok && elect_one()) umma_commit(bar(kBarVEmpty + gl % kVStages));
@@ -624,8 +623,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
     float sl2_next = 0.f;
     float m_run = -INFINITY, l_run = 0.f;  // this row's running max and sum
     auto convert_q = [&](int k) {
-      ok = wait_bar(bar(kBarQFull), k & 1, abort_flag, status);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = wait_bar_warp(bar(kBarQFull), k & 1, abort_flag, status);
       if (!ok) return;
       uint32_t q[D / 2];
       const uint32_t line = sQ + h * LY::kBytes + row * 128;
@@ -683,7 +681,7 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
       const uint32_t g_first = g;
       for (int t = t0; t < t1 && ok; ++t, ++g) {
         // S_h of tile g is complete; so is P.V of tile g-1 (issued before it)
-        ok = wait_bar(bar(kBarSFull + h), g & 1, abort_flag, status);
+        ok = wait_bar_warp(bar(kBarSFull + h), g & 1, abort_flag, status);
         if (!ok) break;
         tc_fence_after();
         uint32_t sr[KT];
@@ -776,14 +774,14 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
         if (elect_one()) mbar_arrive(bar(kBarPFull + h));
       }
       if constexpr (kSplit) {
-        if (ok && t1 > t0) ok = wait_bar(bar(kBarODone + h), (g - 1) & 1, abort_flag, status);
+        if (ok && t1 > t0) ok = wait_bar_warp(bar(kBarODone + h), (g - 1) & 1, abort_flag, status);
         break;  // one item to a cluster
       }
       // the next item's Q while this one's last P.V runs
       if (ok && item_at(k + 1) < num_items) convert_q(k + 1);
       if (!ok || it.ntiles == 0) continue;
       // ---- epilogue: O / l to global memory
-      ok = wait_bar(bar(kBarODone + h), (g - 1) & 1, abort_flag, status);
+      ok = wait_bar_warp(bar(kBarODone + h), (g - 1) & 1, abort_flag, status);
       if (!ok) break;
       tc_fence_after();
       const float inv = v_scale / l_run;
