@@ -120,7 +120,7 @@ enum : int {
   kBarPFull = kBarSFull + 2,
   kBarODone = kBarPFull + 2,
   kBarItem = kBarODone + 2,          // + ring slot of items
-  kBarDrain = kBarItem + 8,          // the MMAs of an issuer that gives up
+  kBarDrain = kBarItem + 8,          // the MMAs under way when a role gave up
   kNumBars
 };
 constexpr int kItemRing = 8;
@@ -600,11 +600,6 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
           __syncwarp();
         }
       }
-      if (!ok) {  // its tensor memory is freed below
-        if (elect_one()) umma_commit(bar(kBarDrain));
-        __syncwarp();
-        drain_bar(bar(kBarDrain), 0, globaltimer());
-      }
     }
   } else {
     // =========================== softmax (two halves) ===========================
@@ -835,8 +830,16 @@ prefill_fp4_kernel(const AttnParams p, const float v_scale, const __grid_constan
   // ---- wind down: every role is done (or gave up); free TMEM
   tc_fence_before();
   __syncthreads();
-  if (sh_abort && threadIdx.x == 0 && sh_loaded >= 0)
-    drain_bar(bar(kBarQFull), sh_loaded & 1, globaltimer());
+  if (sh_abort) {  // whoever gave up: the Q load and the MMAs under way end first
+    if (threadIdx.x == 0 && sh_loaded >= 0)
+      drain_bar(bar(kBarQFull), sh_loaded & 1, globaltimer());
+    if (warp == kWarpMma) {
+      if (elect_one()) umma_commit(bar(kBarDrain));
+      __syncwarp();
+      drain_bar(bar(kBarDrain), 0, globaltimer());
+      __syncwarp();
+    }
+  }
   if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);

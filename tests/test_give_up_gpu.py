@@ -1,8 +1,9 @@
-"""What a warp of the kernels does as it gives up a wait.
+"""What a warp and a role of the kernels do as they give up a wait.
 
-No input of the library reaches that path, so a probe kernel drives the wait of
-``csrc/pa_wait.cuh`` on barriers of its own, with a limit of 1 ms: a warp leaves a wait
-together whatever its lanes saw.
+No input of the library reaches that path, so a probe kernel drives the functions of
+``csrc/pa_wait.cuh`` that it is made of, on barriers of its own, with limits of 1 ms
+and 200 ms: a warp leaves a wait together whatever its lanes saw, and a role that gives
+up waits for what it has under way, but not for ever.
 """
 import ctypes
 import os
@@ -17,6 +18,7 @@ SRC = os.path.join(HERE, "kernels", "give_up_probe.cu")
 OUT = os.path.join(HERE, "_build", "libgive_up_probe.so")
 
 LIMIT_NS = 1_000_000
+OTHER_NS = 200_000_000
 STATUS_WAIT_TIMEOUT = 1   # kStatusWaitTimeout
 
 
@@ -32,7 +34,7 @@ def _probe():
         os.replace(tmp, OUT)
     lib = ctypes.CDLL(OUT)
     lib.give_up_probe.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_ulonglong,
-                                  ctypes.c_int]
+                                  ctypes.c_ulonglong, ctypes.c_int]
     lib.give_up_probe.restype = ctypes.c_int
     return lib
 
@@ -41,7 +43,7 @@ def _run(mode):
     lib = _probe()
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     result = torch.full((34,), -1, dtype=torch.int32, device="cuda")
-    assert lib.give_up_probe(status.data_ptr(), result.data_ptr(), LIMIT_NS, mode) == 0
+    assert lib.give_up_probe(status.data_ptr(), result.data_ptr(), LIMIT_NS, OTHER_NS, mode) == 0
     torch.cuda.synchronize()
     *lanes, aborted, us = result.tolist()
     return int(status.item()), lanes, aborted, us
@@ -59,3 +61,13 @@ def test_a_warp_leaves_a_wait_together():
     assert status == STATUS_WAIT_TIMEOUT and aborted == 1 and us >= LIMIT_NS // 1000
     status, lanes, aborted, us = _run(1)
     assert lanes == [1] * 32 and status == 0 and aborted == 0 and us < LIMIT_NS // 1000
+
+
+@pytest.mark.gpu
+def test_a_role_that_gives_up_waits_for_its_own_work():
+    status, _, aborted, us = _run(2)
+    assert status == 0 and aborted == 1
+    assert LIMIT_NS // 1000 <= us < OTHER_NS // 1000 // 4, "it ends though nothing arrives"
+    status, _, aborted, us = _run(3)
+    assert status == 0 and aborted == 1
+    assert 50 <= us < OTHER_NS // 1000 // 4, "it ends with the arrival, not with the abort flag"
