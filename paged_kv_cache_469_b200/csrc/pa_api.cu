@@ -347,19 +347,15 @@ int attention_impl(void* out, const void* q, const void* k_cache, const void* v_
     }
   }
   if (fork) {
-    if (cudaEventRecord(fork->start, st) != cudaSuccess ||
-        cudaStreamWaitEvent(fork->side, fork->start, 0) != cudaSuccess)
-      return PA_ERR_CUDA;
-    cudaError_t e = launch_prefill_tcgen05(p, head_dim, max_query_len, prefill_items,
-                                           seq_lens_host, query_start_loc_host, fork->side,
-                                           prefill_ctas);
-    if (e != cudaSuccess) return PA_ERR_CUDA;
-    e = launch_decode(p, head_dim, seq_lens_host, query_start_loc_host, st, decode_ctas);
-    if (e != cudaSuccess) return PA_ERR_CUDA;
-    if (cudaEventRecord(fork->done, fork->side) != cudaSuccess ||
-        cudaStreamWaitEvent(st, fork->done, 0) != cudaSuccess)
-      return PA_ERR_CUDA;
-    return PA_OK;
+    auto prefill = [&](cudaStream_t side) {
+      return launch_prefill_tcgen05(p, head_dim, max_query_len, prefill_items, seq_lens_host,
+                                    query_start_loc_host, side, prefill_ctas) == cudaSuccess;
+    };
+    auto decode = [&] {
+      return launch_decode(p, head_dim, seq_lens_host, query_start_loc_host, st, decode_ctas) ==
+             cudaSuccess;
+    };
+    return side_by_side(*fork, st, prefill, decode) ? PA_OK : PA_ERR_CUDA;
   }
   if (any_decode) {
     cudaError_t e = launch_decode(p, head_dim, seq_lens_host, query_start_loc_host, st, sms);

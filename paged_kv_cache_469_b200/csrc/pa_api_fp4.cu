@@ -428,11 +428,8 @@ extern "C" int pa_attention_varlen_fp4(
   ForkStreams* fork = prefill_ctas > 0 ? fork_streams(st) : nullptr;
   if (!fork)
     return (!any_decode || run_decode(sms)) && run_prefill(st, sms) ? PA_OK : PA_ERR_CUDA;
-  if (cudaEventRecord(fork->start, st) != cudaSuccess ||
-      cudaStreamWaitEvent(fork->side, fork->start, 0) != cudaSuccess ||
-      !run_prefill(fork->side, prefill_ctas) || !run_decode(sms - prefill_ctas) ||
-      cudaEventRecord(fork->done, fork->side) != cudaSuccess ||
-      cudaStreamWaitEvent(st, fork->done, 0) != cudaSuccess)
-    return PA_ERR_CUDA;
-  return PA_OK;
+  return side_by_side(*fork, st, [&](cudaStream_t side) { return run_prefill(side, prefill_ctas); },
+                      [&] { return run_decode(sms - prefill_ctas); })
+             ? PA_OK
+             : PA_ERR_CUDA;
 }

@@ -9,6 +9,7 @@
 #include <atomic>
 
 #include "pa.h"
+#include "pa_fork.cuh"
 
 namespace pa {
 
@@ -143,16 +144,6 @@ struct DecodeWork {
 
 // bits of ws_status[0]
 constexpr int kStatusWaitTimeout = 1;  // an mbarrier wait exceeded its time limit
-
-// A side stream and two events, per thread and device, for the calls that run
-// the prefill kernel beside the decode kernel.  Created on the first such call
-// outside a stream capture; a capture that would need to create them runs the
-// kernels one after the other instead.
-struct ForkStreams {
-  cudaStream_t side = nullptr;
-  cudaEvent_t start = nullptr, done = nullptr;
-};
-ForkStreams* fork_streams(cudaStream_t st);
 
 // Workspace layout shared by the size query and the launch.
 struct WorkspaceLayout {
