@@ -1,5 +1,6 @@
 """Build libpa.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc, and the
-Python module ``_binding`` (argument marshalling) with g++.
+Python module ``_binding`` (argument marshalling) with g++.  The library needs nvcc
+alone; where torch is not installed the module, which is of no use there, is left out.
 
     python -m paged_kv_cache_469_b200.build [--force]
 
@@ -54,11 +55,16 @@ def _compile(src: str, force: bool, verbose_ptxas: bool) -> str:
     return obj
 
 
-def _binding(force: bool) -> str:
-    """The Python module, against the installed torch's headers and libraries."""
+def _binding(force: bool) -> str | None:
+    """The Python module, against the installed torch's headers and libraries (None
+    without torch)."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError as e:
+        print(f"_binding left out: {e}", file=sys.stderr)
+        return None
     src = os.path.join(CSRC, "binding.cpp")
     newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "pa.h")))
     if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
@@ -85,7 +91,12 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     with cf.ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
         module = ex.submit(_binding, force)
         objs = list(ex.map(lambda s: _compile(s, force, verbose_ptxas), srcs))
+        _link(objs, force)  # whatever becomes of the module
         module.result()
+    return LIB
+
+
+def _link(objs: list[str], force: bool) -> None:
     if (force or not os.path.exists(LIB)
             or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs)):
         tmp = LIB + f".tmp{os.getpid()}"
@@ -94,7 +105,6 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
