@@ -67,8 +67,15 @@ def _binding(force: bool) -> str | None:
         return None
     src = os.path.join(CSRC, "binding.cpp")
     newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "pa.h")))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
-        return BINDING
+    # an exchanged torch or Python is no newer file: what the module was built for
+    # stands beside the objects
+    mark = os.path.join(BUILD, "binding.built_for")
+    now = f"{torch.__version__} {torch.__file__} {sys.version}"
+    if (not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest
+            and os.path.exists(mark)):
+        with open(mark) as f:
+            if f.read() == now:
+                return BINDING
     root = os.path.dirname(torch.__file__)
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-I", INCLUDE,
@@ -82,6 +89,8 @@ def _binding(force: bool) -> str | None:
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, BINDING)
+    with open(mark, "w") as f:
+        f.write(now)
     return BINDING
 
 

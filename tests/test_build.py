@@ -40,3 +40,27 @@ def test_a_module_that_fails_leaves_the_library_and_says_so(elsewhere, monkeypat
     with pytest.raises(RuntimeError, match="g.. failed"):
         b.build()
     assert loads(b.LIB)
+
+
+def test_the_module_is_built_anew_for_another_torch(elsewhere, monkeypatch):
+    import subprocess
+
+    import torch
+    ran = []
+
+    def run(cmd, **kw):  # a compiler that writes its output at once
+        ran.append(cmd[0])
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+    monkeypatch.setattr(b.subprocess, "run", run)
+    b._binding(True)
+    assert ran == ["g++"] and os.path.exists(b.BINDING)
+    b._binding(False)
+    assert ran == ["g++"], "nothing changed"
+    monkeypatch.setattr(torch, "__version__", "0.0")
+    b._binding(False)
+    b._binding(False)
+    assert ran == ["g++"] * 2
+    os.utime(b.BINDING, (0, 0))  # older than its source
+    b._binding(False)
+    assert ran == ["g++"] * 3
