@@ -130,6 +130,16 @@ PyObject* guarded(Py_ssize_t have, Py_ssize_t want, Body body) {
   return nullptr;
 }
 
+// A call of the C ABI, every argument read: other Python threads run meanwhile (a launch
+// waits while the launch queue is full).
+template <typename Call>
+int unlocked(Call call) {
+  PyThreadState* const state = PyEval_SaveThread();
+  const int status = call();
+  PyEval_RestoreThread(state);
+  return status;
+}
+
 constexpr int kBlockSize = 16;
 
 struct Fp4Cache {
@@ -201,18 +211,26 @@ int append(PyObject* const* args) {
   if (interleaved < 0) throw Refusal{nullptr, ""};
   c10::cuda::CUDAGuard guard(on.device());
   auto* const stream = stream_of(a[5], on.device());
-  if constexpr (kFp4)
-    return api.rope_append_fp4(
-        q_out.data_ptr(), q.const_data_ptr(), qs, k.const_data_ptr(), ks, v.const_data_ptr(), vs,
-        cache.data_ptr(), number(args[4]), number(args[5]), (const int64_t*)slots.const_data_ptr(),
-        positions, angles, longest, rotary, interleaved, t, hq, hkv, d, kBlockSize, num_blocks, dt,
-        stream);
-  else
-    return api.rope_append(q_out.data_ptr(), q.const_data_ptr(), qs, k.const_data_ptr(), ks,
-                           v.const_data_ptr(), vs, cache.data_ptr(),
-                           tensor(args[4], "v_cache").data_ptr(),
-                           (const int64_t*)slots.const_data_ptr(), positions, angles, longest,
-                           rotary, interleaved, t, hq, hkv, d, kBlockSize, num_blocks, dt, stream);
+  void* const to = q_out.data_ptr();
+  const void *const from_q = q.const_data_ptr(), *const from_k = k.const_data_ptr(),
+             *const from_v = v.const_data_ptr();
+  const int64_t* const at = (const int64_t*)slots.const_data_ptr();
+  void* const held = cache.data_ptr();
+  if constexpr (kFp4) {
+    const float k_scale = number(args[4]), v_scale = number(args[5]);
+    return unlocked([&] {
+      return api.rope_append_fp4(to, from_q, qs, from_k, ks, from_v, vs, held, k_scale, v_scale, at,
+                                 positions, angles, longest, rotary, interleaved, t, hq, hkv, d,
+                                 kBlockSize, num_blocks, dt, stream);
+    });
+  } else {
+    void* const held_v = tensor(args[4], "v_cache").data_ptr();
+    return unlocked([&] {
+      return api.rope_append(to, from_q, qs, from_k, ks, from_v, vs, held, held_v, at, positions,
+                             angles, longest, rotary, interleaved, t, hq, hkv, d, kBlockSize,
+                             num_blocks, dt, stream);
+    });
+  }
 }
 
 PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -237,10 +255,16 @@ PyObject* gather_fp4(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const Place on(cache, "kv_cache");
     on.whole(cache, "kv_cache").whole(slots, "slots").whole(k, "k_out").whole(v, "v_out");
     c10::cuda::CUDAGuard guard(on.device());
-    return api.gather_fp4(k.data_ptr(), v.data_ptr(), cache.const_data_ptr(), number(args[2]),
-                          number(args[3]), (const int64_t*)slots.const_data_ptr(),
-                          extent(slots, 0), c.heads, c.d, kBlockSize, c.num_blocks, dt,
-                          stream_of(args[6], on.device()));
+    void *const to_k = k.data_ptr(), *const to_v = v.data_ptr();
+    const void* const from = cache.const_data_ptr();
+    const int64_t* const at = (const int64_t*)slots.const_data_ptr();
+    const float k_scale = number(args[2]), v_scale = number(args[3]);
+    const int n_rows = extent(slots, 0);
+    auto* const stream = stream_of(args[6], on.device());
+    return unlocked([&] {
+      return api.gather_fp4(to_k, to_v, from, k_scale, v_scale, at, n_rows, c.heads, c.d, kBlockSize,
+                            c.num_blocks, dt, stream);
+    });
   });
 }
 
@@ -269,14 +293,25 @@ PyObject* attention_varlen_fp4(PyObject*, PyObject* const* args, Py_ssize_t n) {
     on.whole(q, "q").whole(out, "out").whole(cache, "kv_cache").whole(tables, "block_tables");
     on.whole(lens, "seq_lens").whole(begins, "query_start_loc").whole(ws, "workspace");
     c10::cuda::CUDAGuard guard(on.device());
-    return api.attention_varlen_fp4(
-        out.data_ptr(), q.const_data_ptr(), cache.const_data_ptr(), number(args[3]),
-        number(args[4]), (const int32_t*)tables.const_data_ptr(), extent(tables, 1),
-        (const int32_t*)lens.const_data_ptr(), (const int32_t*)begins.const_data_ptr(),
-        extent(lens, 0), extent(q, 0), small(args[8], "max_query_len"),
-        small(args[9], "max_seq_len"), extent(q, 1), c.heads, c.d, kBlockSize, c.num_blocks,
-        number(args[10]), dt, ws.data_ptr(), ws.nbytes(), (const int32_t*)integer(args[12]),
-        (const int32_t*)integer(args[13]), stream_of(args[14], on.device()));
+    void *const to = out.data_ptr(), *const scratch = ws.data_ptr();
+    const void *const from = q.const_data_ptr(), *const held = cache.const_data_ptr();
+    const int32_t *const blocks = (const int32_t*)tables.const_data_ptr(),
+                  *const lengths = (const int32_t*)lens.const_data_ptr(),
+                  *const starts = (const int32_t*)begins.const_data_ptr();
+    const float k_scale = number(args[3]), v_scale = number(args[4]), scale = number(args[10]);
+    const int wide = extent(tables, 1), seqs = extent(lens, 0), tokens = extent(q, 0),
+              hq = extent(q, 1), max_query_len = small(args[8], "max_query_len"),
+              max_seq_len = small(args[9], "max_seq_len");
+    const auto* const lengths_host = (const int32_t*)integer(args[12]);
+    const auto* const starts_host = (const int32_t*)integer(args[13]);
+    const size_t scratch_bytes = ws.nbytes();
+    auto* const stream = stream_of(args[14], on.device());
+    return unlocked([&] {
+      return api.attention_varlen_fp4(to, from, held, k_scale, v_scale, blocks, wide, lengths,
+                                      starts, seqs, tokens, max_query_len, max_seq_len, hq, c.heads,
+                                      c.d, kBlockSize, c.num_blocks, scale, dt, scratch,
+                                      scratch_bytes, lengths_host, starts_host, stream);
+    });
   });
 }
 
