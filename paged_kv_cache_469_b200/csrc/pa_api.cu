@@ -58,8 +58,15 @@ ForkStreams* fork_streams(cudaStream_t st) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
   ForkStreams& f = per_dev[dev];
-  if (f.side && f.start && f.done) return &f;
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (f.side && f.start && f.done) {
+    // part of a capture that has forked to it, until that ends
+    unsigned long long held = 0, own = 0;
+    if (cudaStreamGetCaptureInfo(f.side, &cs, &held) != cudaSuccess) return nullptr;
+    if (cs == cudaStreamCaptureStatusNone) return &f;
+    if (cudaStreamGetCaptureInfo(st, &cs, &own) != cudaSuccess) return nullptr;
+    return cs == cudaStreamCaptureStatusActive && own == held ? &f : nullptr;
+  }
   if (cudaStreamIsCapturing(st, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone)
     return nullptr;
   if ((!f.side && cudaStreamCreateWithFlags(&f.side, cudaStreamNonBlocking) != cudaSuccess) ||

@@ -9,7 +9,8 @@ namespace pa {
 // A side stream and two events, per thread and device, for the calls that run
 // the prefill kernel beside the decode kernel.  Created on the first such call
 // outside a stream capture; a capture that would need to create them runs the
-// kernels one after the other instead.
+// kernels one after the other instead, and so does a call on any other stream
+// while the side stream is part of a capture.
 struct ForkStreams {
   cudaStream_t side = nullptr;
   cudaEvent_t start = nullptr, done = nullptr;
