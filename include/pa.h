@@ -418,7 +418,8 @@ int pa_rope_append_fp4(void* q_out, const void* q, int64_t q_stride, const void*
  * slots[i] in the pool, k_out[i][h][:] and v_out[i][h][:] are the values of that
  * slot's K and V rows, rounded once to dtype.  Rows of other slots are left as
  * they are.
- *   k_out, v_out  [num_rows][num_kv_heads][head_dim] (written)
+ *   k_out, v_out  [num_rows][num_kv_heads][head_dim] (written); apart from each
+ *                 other and from the cache
  *   slots         int64 [num_rows]
  */
 int pa_gather_fp4(void* k_out, void* v_out, const void* kv_cache, float k_scale, float v_scale,

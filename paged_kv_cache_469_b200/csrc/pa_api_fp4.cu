@@ -271,6 +271,13 @@ extern "C" int pa_gather_fp4(void* k_out, void* v_out, const void* kv_cache, flo
   if (!aligned_to(k_out, 16) || !aligned_to(v_out, 16) || !aligned_to(kv_cache, 16) ||
       !aligned_to(slots, 8))
     return PA_ERR_INVALID;
+  const int elem = dtype == PA_DTYPE_F32 ? 4 : 2;
+  const int64_t row = (int64_t)num_kv_heads * head_dim;
+  const Range out[2] = {rows_range(k_out, num_rows, row, num_kv_heads, head_dim, elem),
+                        rows_range(v_out, num_rows, row, num_kv_heads, head_dim, elem)};
+  const Range cache{kv_cache, (size_t)num_blocks * num_kv_heads * 18 * head_dim};
+  if (out[0].overlaps(out[1]) || out[0].overlaps(cache) || out[1].overlaps(cache))
+    return PA_ERR_INVALID;
   const GatherFp4Params p{k_out,    v_out,        (const uint8_t*)kv_cache, slots,
                           num_rows, num_kv_heads, num_blocks,               k_scale,
                           v_scale};
