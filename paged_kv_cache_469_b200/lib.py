@@ -334,13 +334,15 @@ def rope_append_fp4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_cache:
 def gather_fp4(kv_cache: torch.Tensor, slots: torch.Tensor, *, k_scale: float = 1.0,
                v_scale: float = 1.0, dtype=torch.bfloat16, k_out: torch.Tensor | None = None,
                v_out: torch.Tensor | None = None, stream=None):
-    """K and V values ([n, Hkv, D] each) of the slots (int64 [n]) of a 4-bit cache; rows
-    of slots outside the pool are left as they are (see pa_gather_fp4 in pa.h)."""
+    """K and V values ([n, Hkv, D] each, of ``dtype`` unless one is given) of the slots
+    (int64 [n]) of a 4-bit cache; rows of slots outside the pool are left as they are
+    (see pa_gather_fp4 in pa.h)."""
     if k_out is None or v_out is None:
         shape = (slots.shape[0], kv_cache.shape[1], kv_cache.shape[2] // 18)
         with torch.cuda.stream(stream):  # the fills come before the gather
             if k_out is None:
-                k_out = torch.zeros(shape, dtype=dtype, device=kv_cache.device)
+                k_out = torch.zeros(shape, dtype=dtype if v_out is None else v_out.dtype,
+                                    device=kv_cache.device)
             if v_out is None:
                 v_out = torch.zeros(shape, dtype=k_out.dtype, device=kv_cache.device)
     rc = _marshal().gather_fp4(kv_cache, slots, k_scale, v_scale, k_out, v_out,

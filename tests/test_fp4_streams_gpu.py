@@ -63,3 +63,14 @@ def test_new_memory_is_the_streams_own(make):
     out = call(side)
     side.synchronize()
     assert out.data_ptr() not in taken
+
+
+@pytest.mark.parametrize("which", ["k_out", "v_out"])
+def test_gather_makes_the_output_that_is_not_given_like_the_other(which):
+    tiles = fp4_side.random_tiles(np.random.default_rng(2), 4, 64).reshape(2, 2, 18 * 64)
+    cache, slots = torch.from_numpy(tiles).cuda(), torch.arange(32, device="cuda")
+    want = lib.gather_fp4(cache, slots, dtype=torch.float32)
+    given = torch.zeros_like(want[0])
+    got = lib.gather_fp4(cache, slots, **{which: given})
+    assert given.data_ptr() in (got[0].data_ptr(), got[1].data_ptr())
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
