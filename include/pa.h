@@ -398,7 +398,7 @@ int pa_rope_append(void* q_out, const void* q, int64_t q_stride, const void* k,
  * token's rotated K row, or V row, are stored as
  *   scale = e4m3(min(max|x| / (6 k_scale), 448))     round to nearest even
  *   code  = e2m1(x / (scale * k_scale))              nearest even, at most 6
- * (all codes 0 when the scale rounds to 0, i.e. below 2^-10).  A NaN makes its
+ * (all values 0 when the scale rounds to 0, i.e. from 2^-10 down).  A NaN makes its
  * group's scale NaN; infinities count as the largest value.
  * The bytes of other tokens of a block are left as they are.
  * Arguments as pa_rope_append's; k_scale, v_scale positive and finite.
@@ -453,6 +453,12 @@ size_t pa_attention_fp4_workspace_size(int num_seqs, int num_tokens, int num_q_h
  * query rows, over all SMs; longer prompt chunks run on a tensor-core kernel.
  * The keys of a sequence are cut by the lengths of the whole step: equal steps
  * give equal bits, other companions may change a result's last bits.
+ * Maxima, sums and exponentials are fp32, the products' operands f16.  Codes times
+ * scales are exact there; bf16 queries are down to 2^-17 of their row's largest value,
+ * smaller ones to 2^-25 of it; probabilities are rounded to f16 (2^-11 of each), and the
+ * result once to bf16.  With PA_DTYPE_F32 queries and probabilities are two f16 terms
+ * each: 22 bits where fp32 has 24 (a query value to 2^-25 of its row's largest, if that
+ * is more).
  * Supported: head_dim in {64, 128}; block_size 16; num_q_heads a multiple of
  * num_kv_heads with at most 16 q-heads per kv-head; dtype f32 or bf16; fewer than
  * 2^31 blocks, counted once per sequence, kv-head and 16 query rows (8 where no

@@ -34,10 +34,14 @@
 //
 // Bound: the cache's bytes and the instructions that convert them, together.  192
 // contexts of 256 .. 8192 tokens (32 + 8 heads of 128, 917 MB): 167.5 us, 84 % of
-// the copy rate, issue slots 56 % and the SM clock held down by the power limit; 8
-// of 32768 .. 131072 (855 MB): 152 us, 86 %.  Few short contexts are bound by the
-// chain of dependent reads (lengths, block ids, tiles, parts): one of 77 tokens
-// 7.2 us, 64 of 128 .. 2048 at D = 64 14.5 us.
+// the copy rate, issue slots 56 %, in a short burst; 188 us, 75 %, in a long loop,
+// where the power limit holds the SM clock down; 8 of 32768 .. 131072 (855 MB): 152
+// and 173 us, 86 and 75 %.  At D = 64 a byte takes 1.33 times the instructions: 256 of
+// 8192 (604 MB) 132 and 141 us, 70 and 65 %.  With 16 rows 246 registers leave 8 warps
+// at D = 128: 256 of 16384 on one kv-head (604 MB) 162 and 165 us, 57 %; at D = 64, 512
+// of them 190 us, 49 %.  Few short contexts are bound by the chain of dependent reads
+// (lengths, block ids, tiles, parts): one of 77 tokens 7.2 us, 64 of 128 .. 2048 at
+// D = 64 14.5 us.
 #include <float.h>
 #include <math.h>
 
@@ -101,8 +105,12 @@ struct Shape {
   // Units up to this many blocks are not cut between CTAs: joining a cut unit
   // costs its CTA two more round trips to memory (3 to 5 us, by its rows), the
   // unequal stretches at most this many blocks over the warps of a CTA.  64
-  // contexts of 128 .. 2048 at D = 64, 8 rows: 14.7 us, with half of it 17.0; 33
-  // of 40 .. 3000 with 13 drafted tokens, 16 rows: 18.7, with half of it 21.2.
+  // contexts of 128 .. 2048 at D = 64, 8 rows: 14.2 us, with half of it 16.0, with
+  // half as much again 14.1; 33 of 40 .. 3060 with up to 13 drafted tokens, 16 rows:
+  // 16.4, 18.6 and 16.4.  Around it: 64 of 128 blocks each 14.7 us (half 19.3, more
+  // 14.7), of 129 blocks 18.9 (18.8, 15.2); 33 of 193 blocks, 16 rows, 22.2 (22.2,
+  // 16.9); 30 of 96 and of 97 blocks on 8 kv-heads at D = 128 16.9 and 21.0 (20.5 and
+  // 21.0, 16.9 and 17.5).
   static constexpr int kWhole = R * kWarps;
   // Parts of a unit that one CTA joins at once; of more, groups of so many first.
   // Two steps cost 2 to 4 us more than one of as many parts as that: four

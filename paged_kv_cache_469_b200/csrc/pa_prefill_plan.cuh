@@ -45,8 +45,8 @@ __device__ __forceinline__ int item_index(int k) {
   return k * g + ((k & 1) ? (g - 1 - c) : c);
 }
 
-// One CTA: list the prefill items of every sequence with q_len * group > 64,
-// heaviest (most key tiles) first (a counting sort on the tile count), and
+// One CTA: list the prefill items of every sequence with q_len * group >
+// decode_max_rows, heaviest (most key tiles) first (a counting sort on the tile count), and
 // store the count in ws_items[0].x.  An item pairs two q-heads of one kv-head
 // (pair_heads: the group is even) or two consecutive query tiles of one
 // q-head; its tile count covers the later of its two query tiles.
