@@ -36,7 +36,7 @@
 // contexts of 256 .. 8192 tokens (32 + 8 heads of 128, 917 MB): 167.5 us, 84 % of
 // the copy rate, issue slots 56 %, in a short burst; 188 us, 75 %, in a long loop,
 // where the power limit holds the SM clock down; 8 of 32768 .. 131072 (855 MB): 152
-// and 173 us, 86 and 75 %.  At D = 64 a byte takes 1.33 times the instructions: 256 of
+// and 174 us, 86 and 75 %.  At D = 64 a byte takes 1.33 times the instructions: 256 of
 // 8192 (604 MB) 132 and 141 us, 70 and 65 %.  With 16 rows 246 registers leave 8 warps
 // at D = 128: 256 of 16384 on one kv-head (604 MB) 162 and 165 us, 57 %; at D = 64, 512
 // of them 190 us, 49 %.  Few short contexts are bound by the chain of dependent reads

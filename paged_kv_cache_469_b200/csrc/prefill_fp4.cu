@@ -26,7 +26,7 @@
 // Bound: the softmax's exponentials and the MMAs that wait for them (half of the
 // cycles each), not the cache's bytes.  Four chunks of 1024 over 2712 .. 5048 tokens
 // (32 + 8 heads of 128): 232 us in a short burst, 61 % of the bf16 rate, against 230 of
-// the bf16 prefill kernel on a bf16 cache; 252 us, 56 %, in a long loop.
+// the bf16 prefill kernel on a bf16 cache; 254 us, 56 %, in a long loop.
 //
 // A CTA's first item goes by its number, the others it takes from a counter as
 // the one before has two tiles left: the list is heaviest first, so the CTAs

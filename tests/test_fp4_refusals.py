@@ -27,3 +27,17 @@ def test_gather_outputs_that_overlap(L, dtype, row):
     for bad in (dict(vo=at), dict(vo=at + 2 * row), dict(vo=at - 2 * row), dict(ko=3 << 20),
                 dict(ko=(3 << 20) + 4 * 2304 - 16), dict(vo=(3 << 20) - 2 * row)):
         assert gather(L, dt=dtype, **bad) == palib.PA_ERR_INVALID, bad
+
+
+def test_host_tensors_are_refused_by_name():
+    """Also where the call makes an output of its own first, and on a machine without a
+    GPU."""
+    torch = pytest.importorskip("torch")
+    q, k = torch.zeros(3, 4, 64), torch.zeros(3, 2, 64)
+    kc, cache = torch.zeros(2, 2, 16, 64), torch.zeros(2, 2, 18 * 64, dtype=torch.uint8)
+    slots = torch.zeros(3, dtype=torch.int64)
+    for call in (lambda: palib.rope_append(q, k, k, kc, kc, slots, None, None),
+                 lambda: palib.rope_append_fp4(q, k, k, cache, slots, None, None),
+                 lambda: palib.gather_fp4(cache, slots)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
