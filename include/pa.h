@@ -34,7 +34,8 @@
  *     plan of that call: with the optional host copies of seq_lens and
  *     query_start_loc, that plan follows them (kernel choice, the decode
  *     pieces, their order and their dealing to the CTAs, the prefill work
- *     list), so a replay needs device arrays that still hold those values.
+ *     list), so a replay needs device arrays that still hold those values
+ *     (pa_attention_varlen_fp4: only those of query_start_loc).
  *   - Nothing traps on the device.  Slots or block ids outside the pool are
  *     never dereferenced (see each call).
  *   - dtype is the element type of q, k, v, the caches and out alike.
